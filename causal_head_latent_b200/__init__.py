@@ -23,6 +23,8 @@ __all__ = [
     "gmla_attend_decode", "gmla_attend_decode_workspace_size", "gmla_attend_decode_varlen",
     "gmla_attend_decode_varlen_workspace_size", "gmla_attend_decode_partial", "gmla_attend_decode_partial_workspace_size",
     "gmla_decode_combine", "gmla_attend_decode_noalloc", "gmla_attend_decode_noalloc_max_bytes",
+    "gmla_cache_quantize_fp4", "gmla_cache_dequantize_fp4", "gmla_attend_decode_fp4",
+    "gmla_attend_decode_fp4_workspace_size",
     "gmla_gate_out", "gmla_gate_out_heads", "gmla_gate_out_workspace_size", "gmla_get_device_status",
     "gmla_selftest_wait_timeout", "gmla_status_string",
     "gmla_version", "STATUS",
@@ -89,6 +91,15 @@ lib.gmla_gate_out_heads.argtypes = [_p, _p, _p, _i64, _i64, _i64, _i64, _p, _p, 
 lib.gmla_gate_out_heads.restype = _st
 lib.gmla_gate_out_workspace_size.argtypes = [_i64, _i64]
 lib.gmla_gate_out_workspace_size.restype = _sz
+lib.gmla_cache_quantize_fp4.argtypes = [_p, _i64, _i64, _i64, _i64, _i64, ctypes.c_float, _p, _p, _i64, _i64, _p, _p]
+lib.gmla_cache_quantize_fp4.restype = _st
+lib.gmla_cache_dequantize_fp4.argtypes = [_p, _p, _i64, _i64, _i64, _i64, _i64, ctypes.c_float, _p, _i64, _i64, _p]
+lib.gmla_cache_dequantize_fp4.restype = _st
+lib.gmla_attend_decode_fp4.argtypes = [_p, _p, _p, ctypes.c_float, _i64, _i64, _i64, _p, _i64, _i64, _i64, _p, _p,
+                                       ctypes.c_float, _p, _p, _p, _sz, _p]
+lib.gmla_attend_decode_fp4.restype = _st
+lib.gmla_attend_decode_fp4_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
+lib.gmla_attend_decode_fp4_workspace_size.restype = _sz
 lib.gmla_get_device_status.argtypes = [_p]
 lib.gmla_get_device_status.restype = _st
 lib.gmla_selftest_wait_timeout.argtypes = [ctypes.c_uint, _p]
@@ -362,6 +373,85 @@ def gmla_decode_combine(lse, ctx, W_v, O, G=None, stream=None, check=True):
     code = lib.gmla_decode_combine(_ptr(lse), _ptr(ctx), n_parts, B, H, D, d_c, _ptr(W_v), _ptr(G), _ptr(O),
                                    _stream(stream))
     return _check(code, "gmla_decode_combine") if check else code
+
+
+def _tensor(t, name, dtype, shape):
+    """A contiguous tensor of this type and shape (None in `shape`: any extent) on the current device."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
+    if t.dim() != len(shape) or any(w is not None and int(n) != int(w) for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('any' if w is None else w for w in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must live on the current CUDA device")
+    return t
+
+
+def _fp4_rows(codes, scales):
+    """(B, cache_len_max, d_c) of a 4-bit cache."""
+    _tensor(codes, "codes", torch.uint8, (None, None, None))
+    B, Lmax, half = codes.shape
+    _tensor(scales, "scales", torch.uint8, (B, Lmax, half // 8))
+    return B, Lmax, 2 * half
+
+
+def gmla_cache_quantize_fp4(C, codes, scales, src_row0=0, rows=None, row0=0, row_of=None, cache_scale=1.0, stream=None,
+                            check=True):
+    """Rows src_row0 .. src_row0+rows-1 of C [B, src_len_max, d_c] (all from src_row0 on when rows is None)
+    into rows row0 .. (or row_of[b] .., an int32 tensor on the device) of codes [B, cache_len_max, d_c/2] and
+    scales [B, cache_len_max, d_c/16], both uint8 (see include/gmla.h)."""
+    B, Lmax, d_c = _fp4_rows(codes, scales)
+    _tensor(C, "C", torch.bfloat16, (B, None, d_c))
+    if row_of is not None:
+        _tensor(row_of, "row_of", torch.int32, (B,))
+    n = C.shape[1] - int(src_row0) if rows is None else int(rows)
+    code = lib.gmla_cache_quantize_fp4(_ptr(C), B, C.shape[1], int(src_row0), n, d_c, float(cache_scale), _ptr(codes),
+                                       _ptr(scales), Lmax, int(row0), _ptr(row_of), _stream(stream))
+    return _check(code, "gmla_cache_quantize_fp4") if check else code
+
+
+def gmla_cache_dequantize_fp4(codes, scales, C, row0=0, rows=None, dst_row0=0, cache_scale=1.0, stream=None,
+                              check=True):
+    """Rows row0 .. row0+rows-1 (all from row0 on when rows is None) of a 4-bit cache as bfloat16 rows
+    dst_row0 .. of C [B, dst_len_max, d_c]."""
+    B, Lmax, d_c = _fp4_rows(codes, scales)
+    _tensor(C, "C", torch.bfloat16, (B, None, d_c))
+    n = Lmax - int(row0) if rows is None else int(rows)
+    code = lib.gmla_cache_dequantize_fp4(_ptr(codes), _ptr(scales), B, Lmax, int(row0), n, d_c, float(cache_scale),
+                                         _ptr(C), C.shape[1], int(dst_row0), _stream(stream))
+    return _check(code, "gmla_cache_dequantize_fp4") if check else code
+
+
+def gmla_attend_decode_fp4_workspace_size(B, L, H, d_c) -> int:
+    return lib.gmla_attend_decode_fp4_workspace_size(B, L, H, d_c)
+
+
+def gmla_attend_decode_fp4(Q, codes, scales, L, W_k, W_v, O, num_heads, cache_scale=1.0, lens=None, scale=0.0, G=None,
+                           workspace=None, stream=None, check=True):
+    """Decode over a 4-bit cache: Q, O, G [B, H*D]; rows 0..L-1 visible, or 0..lens[b]-1 with lens an int32
+    tensor of B lengths on the device (at most L)."""
+    B, Lmax, d_c = _fp4_rows(codes, scales)
+    H = int(num_heads)
+    _tensor(Q, "Q", torch.bfloat16, (B, None))
+    d = Q.shape[1]
+    for n, t, shape in (("W_k", W_k, (d, d_c)), ("W_v", W_v, (d, d_c)), ("O", O, (B, d))):
+        _tensor(t, n, torch.bfloat16, shape)
+    if G is not None:
+        _tensor(G, "G", torch.bfloat16, (B, d))
+    if lens is not None:
+        _tensor(lens, "lens", torch.int32, (B,))
+    wp, wb = _ws(workspace)
+    code = lib.gmla_attend_decode_fp4(_ptr(Q), _ptr(codes), _ptr(scales), float(cache_scale), B, Lmax, int(L),
+                                      _ptr(lens), H, _head_width(d, H), d_c, _ptr(W_k), _ptr(W_v), float(scale),
+                                      _ptr(G), _ptr(O), wp, wb, _stream(stream))
+    return _check(code, "gmla_attend_decode_fp4") if check else code
+
+
+def _head_width(d, H):
+    if H < 1 or d % H:
+        raise ValueError(f"num_heads {H} does not divide the model width {d}")
+    return d // H
 
 
 def gmla_gate_out_workspace_size(M, d_model) -> int:

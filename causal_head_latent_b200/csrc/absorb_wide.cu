@@ -1,0 +1,123 @@
+// Absorbed queries for the compact-cache operators, on tcgen05 tensor cores:
+//   q~[b, h, c] = s * sum_r q[b, 128h + r] W_k[128h + r, c]
+// (the decode over 4-bit rows folds scale * log2(e) and the cache's own scale
+// into s).  Same product as the bfloat16 decode's absorb step; what differs is
+// how much of the float32 result is kept:
+//   float16        11 bits, for products with 4-bit rows (which are exact in
+//                  float16); |q~| saturates at 65504
+//   bfloat16 pair  hi = bf16(q~), lo = bf16(q~ - hi): about 16 bits, for the
+//                  accumulated attention weights, whose float32 sums should not
+//                  carry an 8-bit rounding of the query
+// One CTA per (head, 128 latent columns, 32 sequences): D[c, b] = A B with A =
+// 128 columns of W_k^(h) read MN-major, B = the 32 query rows (K-major), K = 128.
+// Bound by latency: each CTA reads 32 KB of W_k once.
+#include "compact.h"
+#include "fp4.cuh"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace gmla {
+namespace absorb_wide {
+
+constexpr int HD = 128;
+constexpr int NB = 32;                // sequences per CTA (the MMA's N)
+constexpr int WCHUNK = 128 * 64 * 2;  // 128 rows x 64 columns of W_k, 128-byte swizzled
+constexpr int QCHUNK = NB * 64 * 2;
+constexpr int THREADS = 128;
+
+struct Smem {
+  uint8_t w[2][WCHUNK];
+  uint8_t q[2][QCHUNK];
+  uint64_t full, done;
+  uint32_t tmem_base;
+};
+static_assert(sizeof(Smem) + 1024 <= 48 * 1024, "fits the default shared-memory limit");
+
+struct Params {
+  uint16_t *f16, *hi, *lo;
+  int B, H, dc;
+  float s;
+  unsigned *status;
+};
+
+__global__ void __launch_bounds__(THREADS)
+    absorb_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmQ, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int h = blockIdx.x, c0 = blockIdx.y * 128, b0 = blockIdx.z * NB;
+  const int nchunk = min(2, (p.dc - c0) / 64);
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full, 1);
+    mbar_init(&sm.done, 1);
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&sm.tmem_base, NB);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  if (threadIdx.x == 0) {
+    mbar_arrive_expect_tx(&sm.full, (uint32_t)(nchunk * WCHUNK + 2 * QCHUNK));
+    for (int k = 0; k < nchunk; ++k) tma_load_2d(sm.w[k], &tmW, &sm.full, c0 + 64 * k, HD * h);
+    for (int j = 0; j < 2; ++j) tma_load_2d(sm.q[j], &tmQ, &sm.full, HD * h + 64 * j, b0);
+    if (mbar_wait(&sm.full, 0, p.status)) {
+      tc_fence_after();
+      constexpr uint32_t idesc = idesc_bf16_f32(128, NB, true, false);
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk)
+        // a missing second W chunk only feeds rows c >= d_c, which are not stored
+        umma_bf16_ss(tmem, sdesc_sw128(smem_u32(sm.w[0]) + kk * 2048, WCHUNK, 1024),
+                     sdesc_sw128(smem_u32(sm.q[kk >> 2]) + (kk & 3) * 32, 16, 1024), idesc, kk > 0);
+    }
+    umma_commit(&sm.done);
+  }
+  __syncwarp();
+  const bool ok = mbar_wait(&sm.done, 0, p.status);
+  tc_fence_after();
+  float v[32];
+  tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), v);
+  const int c = c0 + 32 * warp + lane;
+  if (ok && c < p.dc) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+      if (b0 + j >= p.B) continue;
+      const size_t i = ((size_t)(b0 + j) * p.H + h) * p.dc + c;
+      const float x = v[j] * p.s;
+      if (p.f16) {
+        p.f16[i] = __half_as_ushort(__float2half_rn(x != x ? x : fminf(fmaxf(x, -65504.f), 65504.f)));
+      } else {
+        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+        p.hi[i] = __bfloat16_as_ushort(hi);
+        p.lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(hi)));
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, NB);
+  }
+}
+
+}  // namespace absorb_wide
+
+int launch_absorb_wide(const uint16_t *Q, const uint16_t *Wk, int B, int H, int dc, float s, uint16_t *f16,
+                       uint16_t *hi, uint16_t *lo, unsigned *status, cudaStream_t stream) {
+  using namespace absorb_wide;
+  CUtensorMap tw, tq;
+  const long long dw[2] = {dc, (long long)H * HD}, sw[1] = {dc};
+  const unsigned bw[2] = {64, 128};
+  const long long dq[2] = {(long long)H * HD, B}, sq[1] = {(long long)H * HD};
+  const unsigned bq[2] = {64, NB};
+  if (!make_tmap_bf16(&tw, Wk, 2, dw, sw, bw) || !make_tmap_bf16(&tq, Q, 2, dq, sq, bq)) return -1;
+  const Params p{f16, hi, lo, B, H, dc, s, status};
+  absorb_wide_kernel<<<dim3(H, (dc + 127) / 128, (B + NB - 1) / NB), THREADS, sizeof(Smem) + 1024, stream>>>(tw, tq, p);
+  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+}
+
+}  // namespace gmla

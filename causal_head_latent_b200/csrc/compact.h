@@ -1,0 +1,56 @@
+// Internal launch interfaces of the compact-cache operators.
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gmla {
+
+// The device status word of the current device (null on a CUDA error).
+unsigned *status_ptr();
+
+// ---------------------------------------------------------------- 4-bit rows
+struct Fp4StoreArgs {
+  const uint16_t *C;  // [B, src_len_max, dc]
+  long long B, src_len_max, src_row0, rows;
+  int dc;
+  float inv_cache_scale;
+  uint8_t *codes, *scales;  // [B, cache_len_max, dc/2], [B, cache_len_max, dc/16]
+  long long cache_len_max, row0;
+  const int *row_of;  // optional [B]: first destination row of each sequence
+};
+int launch_fp4_store(const Fp4StoreArgs &a, cudaStream_t stream);
+
+struct Fp4LoadArgs {
+  const uint8_t *codes, *scales;
+  long long B, cache_len_max, row0, rows;
+  int dc;
+  float cache_scale;
+  uint16_t *C;  // [B, dst_len_max, dc]
+  long long dst_len_max, dst_row0;
+};
+int launch_fp4_load(const Fp4LoadArgs &a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- absorbed queries
+// s * W_k^(h)T q_h for every (b, h): as float16 (f16 non-null, saturating) or as
+// a bfloat16 pair hi + lo (about 16 bits); [B, H, dc].
+int launch_absorb_wide(const uint16_t *Q, const uint16_t *Wk, int B, int H, int dc, float s, uint16_t *f16,
+                       uint16_t *hi, uint16_t *lo, unsigned *status, cudaStream_t stream);
+
+// ---------------------------------------------------------------- decode over 4-bit rows
+struct Fp4DecodeArgs {
+  const uint16_t *Q;
+  const uint8_t *codes, *scales;
+  float cache_scale;
+  long long cache_len_max;
+  int B, L, H, dc;
+  const int *lens;  // optional device [B], clamped to 0..L
+  const uint16_t *Wk, *Wv, *G;
+  float scale;
+  uint16_t *O;
+  void *workspace;
+  unsigned *status;
+};
+int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream);
+
+}  // namespace gmla

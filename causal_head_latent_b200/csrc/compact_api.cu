@@ -1,0 +1,93 @@
+// C-ABI entry points of the compact latent cache (declared in include/gmla.h):
+// argument checks on the host, then the launches.
+#include <math.h>
+
+#include "../../include/gmla.h"
+#include "compact.h"
+#include "compact_plan.h"
+
+using namespace gmla;
+
+namespace {
+
+bool aligned(const void *p, size_t a = 16) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool power_of_two(float x) {
+  int e;
+  return x > 0.f && x <= 0x1p64f && x >= 0x1p-64f && frexpf(x, &e) == 0.5f;
+}
+
+constexpr int64_t kMaxBatch = 65535, kMaxRows = int64_t(1) << 25;
+
+bool latent_width_ok(int64_t d_c) { return d_c % 64 == 0 && d_c <= 512; }
+
+// rows [r0, r0 + n) lie in 0..max - 1
+bool range_ok(int64_t r0, int64_t n, int64_t max) { return r0 >= 0 && n >= 1 && r0 <= max && n <= max - r0; }
+
+}  // namespace
+
+extern "C" {
+
+gmla_status gmla_cache_quantize_fp4(const gmla_bf16 *C, int64_t B, int64_t src_len_max, int64_t src_row0, int64_t rows,
+                                    int64_t d_c, float cache_scale, uint8_t *codes, uint8_t *scales,
+                                    int64_t cache_len_max, int64_t row0, const int32_t *row_of, gmla_stream_t stream) {
+  if (!C || !codes || !scales) return GMLA_ERR_ARG;
+  if (B <= 0 || d_c <= 0 || src_len_max <= 0 || cache_len_max <= 0) return GMLA_ERR_ARG;
+  if (!range_ok(src_row0, rows, src_len_max) || (!row_of && !range_ok(row0, rows, cache_len_max))) return GMLA_ERR_ARG;
+  if (!aligned(C) || !aligned(codes) || !aligned(scales) || !aligned(row_of, 4)) return GMLA_ERR_ARG;
+  if (!power_of_two(cache_scale)) return GMLA_ERR_ARG;
+  if (!latent_width_ok(d_c) || B > kMaxBatch || rows >= kMaxRows) return GMLA_ERR_UNSUPPORTED;
+  if (!status_ptr()) return GMLA_ERR_CUDA;
+  Fp4StoreArgs a{};
+  a.C = C; a.B = B; a.src_len_max = src_len_max; a.src_row0 = src_row0; a.rows = rows; a.dc = (int)d_c;
+  a.inv_cache_scale = 1.f / cache_scale;
+  a.codes = codes; a.scales = scales; a.cache_len_max = cache_len_max; a.row0 = row0; a.row_of = row_of;
+  return launch_fp4_store(a, static_cast<cudaStream_t>(stream)) == 0 ? GMLA_OK : GMLA_ERR_CUDA;
+}
+
+gmla_status gmla_cache_dequantize_fp4(const uint8_t *codes, const uint8_t *scales, int64_t B, int64_t cache_len_max,
+                                      int64_t row0, int64_t rows, int64_t d_c, float cache_scale, gmla_bf16 *C,
+                                      int64_t dst_len_max, int64_t dst_row0, gmla_stream_t stream) {
+  if (!C || !codes || !scales) return GMLA_ERR_ARG;
+  if (B <= 0 || d_c <= 0 || dst_len_max <= 0 || cache_len_max <= 0) return GMLA_ERR_ARG;
+  if (!range_ok(row0, rows, cache_len_max) || !range_ok(dst_row0, rows, dst_len_max)) return GMLA_ERR_ARG;
+  if (!aligned(C) || !aligned(codes) || !aligned(scales)) return GMLA_ERR_ARG;
+  if (!power_of_two(cache_scale)) return GMLA_ERR_ARG;
+  if (!latent_width_ok(d_c) || B > kMaxBatch || rows >= kMaxRows) return GMLA_ERR_UNSUPPORTED;
+  if (!status_ptr()) return GMLA_ERR_CUDA;
+  Fp4LoadArgs a{};
+  a.codes = codes; a.scales = scales; a.B = B; a.cache_len_max = cache_len_max; a.row0 = row0; a.rows = rows;
+  a.dc = (int)d_c; a.cache_scale = cache_scale; a.C = C; a.dst_len_max = dst_len_max; a.dst_row0 = dst_row0;
+  return launch_fp4_load(a, static_cast<cudaStream_t>(stream)) == 0 ? GMLA_OK : GMLA_ERR_CUDA;
+}
+
+size_t gmla_attend_decode_fp4_workspace_size(int64_t B, int64_t L, int64_t H, int64_t d_c) {
+  if (B <= 0 || L <= 0 || H <= 0 || d_c <= 0) return 0;
+  return fp4_decode_layout_bytes(B, L, H, d_c);
+}
+
+gmla_status gmla_attend_decode_fp4(const gmla_bf16 *Q, const uint8_t *codes, const uint8_t *scales, float cache_scale,
+                                   int64_t B, int64_t cache_len_max, int64_t L, const int32_t *lens, int64_t H,
+                                   int64_t D_h, int64_t d_c, const gmla_bf16 *W_k, const gmla_bf16 *W_v, float scale,
+                                   const gmla_bf16 *G, gmla_bf16 *O, void *workspace, size_t workspace_bytes,
+                                   gmla_stream_t stream) {
+  if (!Q || !codes || !scales || !W_k || !W_v || !O) return GMLA_ERR_ARG;
+  if (B <= 0 || H <= 0 || D_h <= 0 || d_c <= 0 || L < 1 || cache_len_max < L) return GMLA_ERR_ARG;
+  const void *ptrs[] = {Q, codes, scales, W_k, W_v, G, O, workspace};
+  for (const void *p : ptrs)
+    if (!aligned(p)) return GMLA_ERR_ARG;
+  if (!aligned(lens, 4) || !power_of_two(cache_scale)) return GMLA_ERR_ARG;
+  if (D_h != 128 || !latent_width_ok(d_c) || H > 96) return GMLA_ERR_UNSUPPORTED;
+  if (B > kMaxBatch || L > 0x7fffff00LL) return GMLA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < gmla_attend_decode_fp4_workspace_size(B, L, H, d_c)) return GMLA_ERR_WORKSPACE;
+  if (scale <= 0.f) scale = 1.0f / sqrtf((float)D_h);
+  unsigned *st = status_ptr();
+  if (!st) return GMLA_ERR_CUDA;
+  Fp4DecodeArgs a{};
+  a.Q = Q; a.codes = codes; a.scales = scales; a.cache_scale = cache_scale; a.cache_len_max = cache_len_max;
+  a.B = (int)B; a.L = (int)L; a.H = (int)H; a.dc = (int)d_c; a.lens = lens;
+  a.Wk = W_k; a.Wv = W_v; a.G = G; a.scale = scale; a.O = O; a.workspace = workspace; a.status = st;
+  return launch_attend_fp4(a, static_cast<cudaStream_t>(stream)) == 0 ? GMLA_OK : GMLA_ERR_CUDA;
+}
+
+}  // extern "C"

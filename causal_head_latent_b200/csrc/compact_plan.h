@@ -1,0 +1,64 @@
+// Launch plans and workspace layouts of the compact-cache operators (decode over
+// 4-bit rows, accumulated weights, eviction): integer arithmetic without CUDA
+// types, used by host and device code and checked on the CPU by the tests.
+#pragma once
+#include <stddef.h>
+#include <stdint.h>
+
+#include "ws_layout.h"
+
+#ifdef __CUDACC__
+#define GMLA_PLAN_HD __host__ __device__
+#else
+#define GMLA_PLAN_HD
+#endif
+
+namespace gmla {
+
+constexpr int kFp4TileKeys = 64;     // cached rows per tile of the 4-bit decode
+
+// The tiles of all sequences, laid end to end, are cut into G equal shares, one
+// per CTA, whatever the lengths: CTA i works tiles [share_begin(i), share_begin(i+1)).
+// The lengths live on the device, so G and every buffer depend on sizes alone.
+constexpr int kShares = 148;  // one CTA per SM of a B200
+
+inline long long share_count(long long B, long long L, int tile) {
+  const long long tiles = B * ((L + tile - 1) / tile);
+  return tiles < kShares ? (tiles < 1 ? 1 : tiles) : kShares;
+}
+GMLA_PLAN_HD inline long long share_begin(long long i, long long tiles, long long G) { return i * tiles / G; }
+// The share that holds tile t: the largest i with share_begin(i) <= t.
+GMLA_PLAN_HD inline long long share_of(long long t, long long tiles, long long G) {
+  return ((t + 1) * G - 1) / tiles;
+}
+// Share i's piece of sequence b keeps its partial state in record i + b: along the
+// tiles i and b only grow and every new piece has a larger i or b, so no two pieces
+// share a record, and G + B - 1 records hold them all.
+inline long long share_records(long long B, long long L, int tile) { return share_count(B, L, tile) + B - 1; }
+
+// 4-bit decode: q~ float16 [B,H,dc] | m, l float [R,H] | acc float [R,H,dc] | c^ float [B,H,dc].
+struct Fp4DecodeLayout {
+  size_t qt, pm, pl, pacc, chat, end;
+};
+inline Fp4DecodeLayout fp4_decode_layout(uintptr_t base, long long B, long long L, long long H, long long dc) {
+  const size_t R = (size_t)share_records(B, L, kFp4TileKeys);
+  Fp4DecodeLayout o;
+  size_t off = ws_round(base) - base;
+  o.qt = off;
+  off += ws_round(2 * (size_t)B * H * dc);
+  o.pm = off;
+  off += ws_round(4 * R * H);
+  o.pl = off;
+  off += ws_round(4 * R * H);
+  o.pacc = off;
+  off += ws_round(4 * R * H * dc);
+  o.chat = off;
+  off += ws_round(4 * (size_t)B * H * dc);
+  o.end = off;
+  return o;
+}
+inline size_t fp4_decode_layout_bytes(long long B, long long L, long long H, long long dc) {
+  return (kWsAlign - 16) + fp4_decode_layout(0, B, L, H, dc).end;
+}
+
+}  // namespace gmla

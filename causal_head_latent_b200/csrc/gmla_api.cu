@@ -11,6 +11,7 @@
 #include "../../include/gmla.h"
 #include <vector>
 
+#include "compact.h"
 #include "internal.h"
 #include "ptx.cuh"
 #include "ws_layout.h"
@@ -65,7 +66,7 @@ bool set_smem_limit_once(const void *kernel, int bytes, SmemSlot slot) {
   return true;
 }
 
-static unsigned *status_ptr() {
+unsigned *status_ptr() {
   const int d = current_device();
   if (!device_setup(d)) return nullptr;
   return g_status_ptr[d];

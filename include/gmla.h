@@ -31,6 +31,10 @@
  *                            cached rows (context-parallel decode) ...
  *  gmla_decode_combine       ... and the exact merge of such states into the output
  *  gmla_attend_decode_noalloc  gmla_attend_decode without a caller workspace
+ *  gmla_cache_quantize_fp4   latent rows held in 4 bits (288 bytes instead of 1024 at
+ *                            d_c = 512), and back:
+ *  gmla_cache_dequantize_fp4   bfloat16 rows of a range of 4-bit rows
+ *  gmla_attend_decode_fp4    gmla_attend_decode over 4-bit rows
  *  gmla_gate_out             the gate and output projection Y = (sigmoid(G) (.) O) W_o^T
  *  gmla_gate_out_heads       its share for a range of heads (head-parallel prefill)
  *  gmla_get_device_status, gmla_selftest_wait_timeout, gmla_status_string,
@@ -422,6 +426,77 @@ GMLA_API size_t gmla_gate_out_workspace_size(int64_t M, int64_t d_model);
 GMLA_API gmla_status gmla_gate_out_heads(const gmla_bf16 *O, const gmla_bf16 *G, const gmla_bf16 *W_o, int64_t M,
                                         int64_t d_model, int64_t head_begin, int64_t head_end, gmla_bf16 *Y,
                                         void *workspace, size_t workspace_bytes, gmla_stream_t stream);
+
+/*
+ * gmla_cache_quantize_fp4 -- latent rows stored in 4 bits.
+ *
+ * A row of d_c channels is cut into groups of 16.  A group is held as 16 codes
+ * e (e2m1: a sign and a magnitude of 0, 0.5, 1, 1.5, 2, 3, 4 or 6) and one
+ * scale s (e4m3, positive), and stands for c_i = cache_scale * s * e_i:
+ *     s   = e4m3(max(min(max_i |x_i|, 2688) / 6, 2^-9)),   x_i = C_i / cache_scale
+ *     e_i = e2m1(x_i / s)
+ * both rounded to nearest, ties to even; magnitudes above 6 s become 6 s, a NaN
+ * is held as 0 and -0 as 0.  s * e has at most 6 significant bits, so reading a
+ * row back adds no further rounding.  9/32 of a bfloat16 row's bytes.
+ *
+ *  C       [B, src_len_max, d_c]; rows [src_row0, src_row0 + rows) are stored
+ *  codes   [B, cache_len_max, d_c / 2] bytes; channel 2i in the low half of byte i
+ *  scales  [B, cache_len_max, d_c / 16] bytes
+ *  row0    destination of the first row of every sequence, unless row_of is given:
+ *  row_of  optional DEVICE array of B int32: sequence b's rows go to row_of[b] + t
+ *          (a decode step of sequences of different lengths appends with
+ *          rows = 1, row_of = lengths).  Rows that fall outside
+ *          0..cache_len_max - 1 are dropped.  Read when the kernel runs, so a
+ *          captured call follows the array's current values.
+ *  cache_scale  a power of two between 2^-64 and 2^64, the same for every call on
+ *          this cache; 1 suits latents of unit size (s spans 2^-9 to 448).
+ * Only the rows stored are written.  Errors: GMLA_ERR_ARG for null or misaligned
+ * pointers, ranges outside the arrays, or a cache_scale that is not such a power
+ * of two; GMLA_ERR_UNSUPPORTED when d_c is not a multiple of 64 or above 512, or
+ * B > 65535, or a sequence's range has 2^25 rows or more.
+ */
+GMLA_API gmla_status gmla_cache_quantize_fp4(const gmla_bf16 *C, int64_t B, int64_t src_len_max, int64_t src_row0,
+                                             int64_t rows, int64_t d_c, float cache_scale, uint8_t *codes,
+                                             uint8_t *scales, int64_t cache_len_max, int64_t row0,
+                                             const int32_t *row_of, gmla_stream_t stream);
+
+/*
+ * gmla_cache_dequantize_fp4 -- rows [row0, row0 + rows) of a 4-bit cache as
+ * bfloat16 rows [dst_row0, dst_row0 + rows) of C [B, dst_len_max, d_c], exactly
+ * the values they stand for: what gmla_expand_kv needs of a cached prefix when a
+ * prefill chunk continues it.  Only those rows of C are written.  Errors as
+ * gmla_cache_quantize_fp4.
+ */
+GMLA_API gmla_status gmla_cache_dequantize_fp4(const uint8_t *codes, const uint8_t *scales, int64_t B,
+                                               int64_t cache_len_max, int64_t row0, int64_t rows, int64_t d_c,
+                                               float cache_scale, gmla_bf16 *C, int64_t dst_len_max,
+                                               int64_t dst_row0, gmla_stream_t stream);
+
+/*
+ * gmla_attend_decode_fp4 -- gmla_attend_decode over a cache held in 4 bits
+ * (gmla_cache_quantize_fp4): one new query per sequence, the same absorbed
+ * evaluation, with c_s the rows that codes and scales stand for.
+ *
+ *  codes   [B, cache_len_max, d_c / 2], scales [B, cache_len_max, d_c / 16]
+ *  L       rows 0..L-1 of every sequence are visible, 1 <= L <= cache_len_max,
+ *          unless lens is given:
+ *  lens    optional DEVICE array of B int32: rows 0..lens[b]-1 of sequence b are
+ *          visible, lens[b] clamped to 0..L (L then bounds the lengths and the
+ *          launch).  A sequence of length 0 gets O = 0.  Read when the kernels
+ *          run, so a captured call follows the array's current values.
+ *  Rows that are not visible are never read.
+ *  Q, W_k, W_v, scale, G, O as gmla_attend_decode.
+ *  workspace >= gmla_attend_decode_fp4_workspace_size(B, L, H, d_c) bytes, 16-byte
+ *          aligned.  Calls that may overlap on the GPU need one each.
+ * Errors as gmla_attend_decode; GMLA_ERR_ARG also for a bad cache_scale.
+ */
+GMLA_API gmla_status gmla_attend_decode_fp4(const gmla_bf16 *Q, const uint8_t *codes, const uint8_t *scales,
+                                            float cache_scale, int64_t B, int64_t cache_len_max, int64_t L,
+                                            const int32_t *lens, int64_t H, int64_t D_h, int64_t d_c,
+                                            const gmla_bf16 *W_k, const gmla_bf16 *W_v, float scale,
+                                            const gmla_bf16 *G, gmla_bf16 *O, void *workspace,
+                                            size_t workspace_bytes, gmla_stream_t stream);
+GMLA_API size_t gmla_attend_decode_fp4_workspace_size(int64_t B, int64_t L, int64_t H, int64_t d_c);
 
 /* Synchronise `stream`, then read and clear this device's status word.
  * Returns GMLA_OK, GMLA_ERR_TIMEOUT (a bounded wait ran out) or GMLA_ERR_CUDA. */
