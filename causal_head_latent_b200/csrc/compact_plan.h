@@ -15,7 +15,7 @@
 
 namespace gmla {
 
-constexpr int kFp4TileKeys = 64;     // cached rows per tile of the 4-bit decode
+constexpr int kFp4TileKeys = 48;     // cached rows per tile of the 4-bit decode
 
 // The tiles of all sequences, laid end to end, are cut into G equal shares, one
 // per CTA, whatever the lengths: CTA i works tiles [share_begin(i), share_begin(i+1)).

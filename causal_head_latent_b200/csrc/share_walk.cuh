@@ -99,6 +99,16 @@ struct ShareWalk {
     }
     return false;
   }
+  // next() for a whole converged warp: lane 0's answer in every lane, so that what is
+  // computed from it stays in uniform registers.
+  __device__ __forceinline__ bool next_uniform(const ShareBatch &s, SharePiece *p) {
+    const bool more = __shfl_sync(0xffffffffu, (int)next(s, p), 0) != 0;
+    p->b = __shfl_sync(0xffffffffu, p->b, 0);
+    p->tile0 = __shfl_sync(0xffffffffu, p->tile0, 0);
+    p->n = __shfl_sync(0xffffffffu, p->n, 0);
+    p->len = __shfl_sync(0xffffffffu, p->len, 0);
+    return more;
+  }
 };
 
 }  // namespace gmla

@@ -55,7 +55,7 @@ static int shares(const std::vector<long long> &lens, long long L, int tile) {
 }
 int main() {
   std::srand(1);
-  for (int tile : {64, 128}) {
+  for (int tile : {48, 128}) {
     for (long long B : {1, 2, 3, 32, 147, 148, 149, 500})
       for (long long L : {1, 63, 64, 65, 1000, 5000})
         for (int kind = 0; kind < 4; ++kind) {
