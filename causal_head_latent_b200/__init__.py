@@ -24,7 +24,7 @@ __all__ = [
     "gmla_attend_decode_varlen_workspace_size", "gmla_attend_decode_partial", "gmla_attend_decode_partial_workspace_size",
     "gmla_decode_combine", "gmla_attend_decode_noalloc", "gmla_attend_decode_noalloc_max_bytes",
     "gmla_cache_quantize_fp4", "gmla_cache_dequantize_fp4", "gmla_attend_decode_fp4",
-    "gmla_attend_decode_fp4_workspace_size",
+    "gmla_attend_decode_fp4_workspace_size", "gmla_cache_score", "gmla_cache_score_workspace_size",
     "gmla_gate_out", "gmla_gate_out_heads", "gmla_gate_out_workspace_size", "gmla_get_device_status",
     "gmla_selftest_wait_timeout", "gmla_status_string",
     "gmla_version", "STATUS",
@@ -100,6 +100,11 @@ lib.gmla_attend_decode_fp4.argtypes = [_p, _p, _p, ctypes.c_float, _i64, _i64, _
 lib.gmla_attend_decode_fp4.restype = _st
 lib.gmla_attend_decode_fp4_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
 lib.gmla_attend_decode_fp4_workspace_size.restype = _sz
+lib.gmla_cache_score.argtypes = [_p, _p, _i64, _i64, _i64, _p, _i64, _i64, _i64, _p, ctypes.c_float, ctypes.c_float,
+                                 _p, _p, _sz, _p]
+lib.gmla_cache_score.restype = _st
+lib.gmla_cache_score_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
+lib.gmla_cache_score_workspace_size.restype = _sz
 lib.gmla_get_device_status.argtypes = [_p]
 lib.gmla_get_device_status.restype = _st
 lib.gmla_selftest_wait_timeout.argtypes = [ctypes.c_uint, _p]
@@ -446,6 +451,30 @@ def gmla_attend_decode_fp4(Q, codes, scales, L, W_k, W_v, O, num_heads, cache_sc
                                       _ptr(lens), H, _head_width(d, H), d_c, _ptr(W_k), _ptr(W_v), float(scale),
                                       _ptr(G), _ptr(O), wp, wb, _stream(stream))
     return _check(code, "gmla_attend_decode_fp4") if check else code
+
+
+def gmla_cache_score_workspace_size(B, L, H, d_c) -> int:
+    return lib.gmla_cache_score_workspace_size(B, L, H, d_c)
+
+
+def gmla_cache_score(Q, C, L, W_k, score, num_heads, lens=None, scale=0.0, decay=1.0, workspace=None, stream=None,
+                     check=True):
+    """score [B, cache_len_max] float32 = decay * score + the attention weight of every visible row, summed over
+    heads: Q [B, H*D]; C [B, cache_len_max, d_c]; rows 0..L-1 visible, or 0..lens[b]-1 with lens an int32 tensor of
+    B lengths on the device (at most L)."""
+    _tensor(C, "C", torch.bfloat16, (None, None, None))
+    B, Lmax, d_c = C.shape
+    H = int(num_heads)
+    _tensor(Q, "Q", torch.bfloat16, (B, None))
+    d = Q.shape[1]
+    _tensor(W_k, "W_k", torch.bfloat16, (d, d_c))
+    _tensor(score, "score", torch.float32, (B, Lmax))
+    if lens is not None:
+        _tensor(lens, "lens", torch.int32, (B,))
+    wp, wb = _ws(workspace)
+    code = lib.gmla_cache_score(_ptr(Q), _ptr(C), B, Lmax, int(L), _ptr(lens), H, _head_width(d, H), d_c, _ptr(W_k),
+                                float(scale), float(decay), _ptr(score), wp, wb, _stream(stream))
+    return _check(code, "gmla_cache_score") if check else code
 
 
 def _head_width(d, H):

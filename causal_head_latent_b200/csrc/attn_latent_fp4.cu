@@ -138,13 +138,6 @@ __device__ __forceinline__ void bar_sync(int id, int count) {
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
-// Waits of a whole converged warp; every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned *status) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status)) != 0;
-}
-__device__ __forceinline__ bool warp_wait_relaxed(uint64_t *bar, uint32_t parity, unsigned *status) {
-  return __all_sync(0xffffffffu, mbar_wait_relaxed(bar, parity, status)) != 0;
-}
 // Whether some head raised its maximum in tile g (after p_full of g).
 __device__ __forceinline__ bool asks_rescale(const volatile int *rescale_s, int nq, int g) {
   bool any = false;

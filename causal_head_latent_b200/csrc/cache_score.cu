@@ -1,0 +1,421 @@
+// Accumulated attention weight of every cached row (what an eviction goes by):
+//   score[b, s] = decay * score[b, s] + sum_h a_bhs,   a_bh = softmax_s(q~_bh . c_bs),
+// for one new query per sequence over the bfloat16 latent cache, with q~ the absorbed
+// query (log2(e) / sqrt(D) folded in).  The sum runs over steps in float32, so one step's
+// weights should not carry bfloat16's 8 bits: q~ goes in as hi + lo (about 16 bits) and
+//   S = hi C^T + lo C^T
+// on tcgen05 tensor cores, float32 accumulators; the rows c are bfloat16 as they are.
+//
+// Two launches per group of sequences.
+//  scores_kernel   S of every (head, row), stored as float32, and per piece the running
+//                  maximum and sum of 2^S of every head;
+//  sum_kernel      the pieces' states joined into each head's log-sum-exp, then
+//                  sum_h 2^(S - lse_h) per row, added to the score.
+// The weights of a row need every head's log-sum-exp, hence all rows: either the rows are
+// read twice (2 * 1024 bytes at d_c = 512) or S goes out and in (1024 + 2 * 384 at 96
+// heads, and no second run of the MMAs).  S passes through at most 256 MB of workspace,
+// a group of sequences at a time.
+//
+// scores_kernel.  One CTA per SM, an equal share of the group's 128-row tiles each
+// (compact_plan.h).  HBM bounds it: 1 KB a row, 44 cycles a row at an SM's share of the
+// bandwidth; the MMAs take 32: 64 a tile (M = 128 heads, padded by overlap; N = 128 rows;
+// hi from shared memory, lo as a tensor-memory operand, because two copies of q~ would
+// leave 32 KB for the rows; so the ring holds eight 16 KB chunks, a whole tile).
+//   warp 0       TMA of the rows, 64-column chunks
+//   warp 1       TMEM owner; issues the MMAs (converged, one lane predicated)
+//   warp 2       TMA of q~ hi
+//   warps 4..7   q~ lo into TMEM; per tile the running softmax state and the store of S
+// TMEM: D buffers at columns 0 and 128, q~ lo at 256 (a column holds two elements).
+#include <math.h>
+
+#include "compact.h"
+#include "compact_plan.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "share_walk.cuh"
+
+namespace gmla {
+namespace cache_score {
+
+constexpr int HMAX = 96;
+constexpr int KT = kScoreTileKeys;
+constexpr int NUM_THREADS = 256;
+constexpr int NCHUNK = 8;                   // 64-wide d_c chunks (d_c <= 512)
+constexpr int QCHUNK = HMAX * 128;          // rows 96..127 of a 128-row A tile alias what follows: S rows nobody reads
+constexpr int Q_BYTES = NCHUNK * QCHUNK;
+constexpr int CCHUNK = KT * 128;            // 128 rows x 64 columns
+constexpr int NSLOT = 8;
+constexpr int TM_D = 0, TM_LO = 256;
+constexpr unsigned long long kDrainLimitNs = 100000000ull;
+static_assert(CCHUNK >= 32 * 128, "the first ring slot covers the q~ tail");
+
+struct Params {
+  int H, dc, Hp;            // Hp: heads rounded up to 32
+  long long tiles_max;      // tiles of a sequence in S
+  ShareBatch batch;
+  const uint16_t *lo;       // [B, H, dc]
+  float *part_m, *part_l;   // [R, H]
+  float *S;                 // [B][tiles_max][KT / 4][Hp][4]
+  unsigned *status;
+};
+
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    scores_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC, const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t *sq = smem, *sc = sq + Q_BYTES;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sc + NSLOT * CCHUNK);  // [NSLOT]
+  uint64_t *empty = full + NSLOT;                                      // [NSLOT]
+  uint64_t *d_full = empty + NSLOT;                                    // [2]
+  uint64_t *d_free = d_full + 2;                                       // [2]
+  uint64_t *q_full = d_free + 2, *q_free = q_full + 1, *lo_full = q_full + 2, *idle = q_full + 3;
+  long long *sums = reinterpret_cast<long long *>(idle + 1);  // [2]
+  int *start = reinterpret_cast<int *>(sums + 2);             // [2]
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 2);
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  const ShareBatch batch = p.batch;
+  long long unused, total;
+  block_tile_sums(batch, 0, sums, &unused, &total);
+  const long long G = min((long long)gridDim.x, total);
+  if (blockIdx.x >= G) return;  // the whole CTA, before any barrier
+  const long long t0 = share_begin(blockIdx.x, total, G);
+  const int n_all = (int)(share_begin(blockIdx.x + 1, total, G) - t0);
+  const int nchunk = p.dc / 64;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NSLOT; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&d_full[i], 1);
+      mbar_init(&d_free[i], 4);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_free, 1);
+    mbar_init(lo_full, 4);
+    mbar_init(idle, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 3) {
+    int fb, ft;
+    warp_find_tile(batch, t0, &fb, &ft);
+    if (lane == 0) {
+      start[0] = fb;
+      start[1] = ft;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  ShareWalk walk{start[0], start[1], n_all};
+  SharePiece pc{};
+
+  if (warp == 0) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmC);
+      int c = 0;
+      bool ok = true;
+      while (ok && walk.next(batch, &pc)) {
+        for (int j = 0; ok && j < pc.n; ++j) {
+          for (int kc = 0; kc < nchunk; ++kc, ++c) {
+            const int slot = c % NSLOT;
+            if (c >= NSLOT && !mbar_wait(&empty[slot], (c / NSLOT - 1) & 1, p.status)) {
+              ok = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&full[slot], CCHUNK);
+            tma_load_3d(sc + slot * CCHUNK, &tmC, &full[slot], kc * 64, (pc.tile0 + j) * KT, pc.b);
+          }
+        }
+      }
+      // no copy is in flight when this thread leaves, whatever the others do
+      for (int k = max(0, c - NSLOT); k < c; ++k)
+        mbar_wait_limit(&full[k % NSLOT], (k / NSLOT) & 1, p.status, kDrainLimitNs);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    const uint32_t issue = elect_one();
+    constexpr uint32_t id = idesc_bf16_f32(128, KT, false, false);
+    const uint32_t aq = smem_u32(sq), ac = smem_u32(sc);
+    bool ok = true;
+    int c = 0;
+    for (int i = 0, g = 0; ok && walk.next_uniform(batch, &pc); ++i) {
+      ok = warp_wait(q_full, i & 1, p.status) && warp_wait(lo_full, i & 1, p.status);
+      for (int j = 0; ok && j < pc.n; ++j, ++g) {
+        if (g >= 2) ok = warp_wait_relaxed(&d_free[g & 1], ((g - 2) >> 1) & 1, p.status);
+        const uint32_t d = tmem + TM_D + (g & 1) * 128;
+        for (int kc = 0; ok && kc < nchunk; ++kc, ++c) {
+          const int slot = c % NSLOT;
+          ok = warp_wait_relaxed(&full[slot], (c / NSLOT) & 1, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = aq + kc * QCHUNK, b = ac + slot * CCHUNK, alo = tmem + TM_LO + kc * 32;
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            const uint64_t db = sdesc_sw128(b + kk * 32, 16, 1024);
+            umma_f16_ss_if(issue, d, sdesc_sw128(a + kk * 32, 16, 1024), db, id, (kc | kk) ? 1u : 0u);
+            umma_f16_ts_if(issue, d, alo + kk * 8, db, id, 1u);
+          }
+          umma_commit_if(issue, &empty[slot]);
+        }
+        if (!ok) break;
+        umma_commit_if(issue, &d_full[g & 1]);
+      }
+      if (ok) umma_commit_if(issue, q_free);
+    }
+    if (issue) {
+      umma_commit(idle);
+      mbar_wait_limit(idle, 0, p.status, kDrainLimitNs);
+    }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      tma_prefetch_desc(&tmQ);
+      for (int i = 0; walk.next(batch, &pc); ++i) {
+        if (i > 0 && !mbar_wait(q_free, (i - 1) & 1, p.status)) break;
+        mbar_arrive_expect_tx(q_full, nchunk * QCHUNK);
+        for (int kc = 0; kc < nchunk; ++kc) tma_load_3d(sq + kc * QCHUNK, &tmQ, q_full, kc * 64, 0, pc.b);
+        if (!mbar_wait_limit(q_full, i & 1, p.status, kDrainLimitNs)) break;
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax state, S
+    const int quarter = warp & 3, h = quarter * 32 + lane;  // TMEM lane = head
+    const bool head_ok = h < p.H;
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    bool ok = true;
+    for (int i = 0, g = 0; ok && walk.next(batch, &pc); ++i) {
+      // q~ lo of the piece (the MMAs of the piece before are done: its last d_full was waited for)
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.lo + ((size_t)pc.b * p.H + (head_ok ? h : 0)) * p.dc);
+      for (int kc = 0; kc < nchunk; ++kc) {
+        float v[32];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint4 w = head_ok ? src[kc * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
+          v[4 * k] = __uint_as_float(w.x);
+          v[4 * k + 1] = __uint_as_float(w.y);
+          v[4 * k + 2] = __uint_as_float(w.z);
+          v[4 * k + 3] = __uint_as_float(w.w);
+        }
+        tmem_st32(tmem + lane_off + TM_LO + kc * 32, v);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(lo_full);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < pc.n; ++j, ++g) {
+        ok = warp_wait(&d_full[g & 1], (g >> 1) & 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        const int left = pc.len - (pc.tile0 + j) * KT;  // visible rows of this tile
+        float4 *out = reinterpret_cast<float4 *>(p.S) +
+                      (((size_t)pc.b * p.tiles_max + pc.tile0 + j) * (KT / 4)) * p.Hp + h;
+#pragma unroll 1
+        for (int c0 = 0; c0 < KT; c0 += 32) {
+          float x[32];
+          if (quarter * 32 < p.H) tmem_ld32(tmem + lane_off + TM_D + (g & 1) * 128 + c0, x);
+          if (c0 + 32 == KT) {  // the last read of this D buffer
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_free[g & 1]);
+          }
+          if (head_ok && left > c0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              out[(size_t)(c0 / 4 + k) * p.Hp] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            if (left < c0 + 32) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (c0 + k >= left) x[k] = -INFINITY;
+            }
+            float mx = m;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, x[k]);
+            if (mx > m) {
+              l *= m == -INFINITY ? 0.f : fast_exp2(m - mx);
+              m = mx;
+            }
+            float rs[4] = {0.f, 0.f, 0.f, 0.f};
+            const float mref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) rs[k & 3] += fast_exp2(x[k] - mref);
+            l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
+          }
+          __syncwarp();
+        }
+      }
+      if (ok && head_ok) {
+        const size_t rec = ((size_t)blockIdx.x + pc.b) * p.H + h;
+        p.part_m[rec] = m;
+        p.part_l[rec] = l;
+      }
+    }
+    tc_fence_before();
+  }
+
+  __syncwarp();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + 8 * (2 * NSLOT + 8) + 16 + 8 + 16; }
+static_assert(smem_bytes() <= 232448, "dynamic shared memory above the 227 KB a CTA may have");
+
+// Log-sum-exp per head from the pieces' states, then sum_h 2^(S - lse_h) per row.  A block
+// takes `per_block` tiles of a sequence (blockIdx.y); a warp takes sixteen rows at a time, in
+// quads, its lanes the heads, so that S is read in whole 512-byte lines, twelve in flight.
+constexpr int ST = 256;
+
+struct SumParams {
+  ShareBatch batch;
+  long long G, tiles_max;
+  int H, Hp;
+  const float *part_m, *part_l, *S;
+  float decay;
+  float *score;
+  long long score_ld;
+  int per_block;
+};
+
+__global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
+  __shared__ long long sums[2];
+  __shared__ float m_s[ST], l_s[ST], lse_s[128];
+  const int b = blockIdx.y;
+  long long before, total;
+  block_tile_sums(p.batch, b, sums, &before, &total);
+  const int len = p.batch.len(b), n = p.batch.tiles(b), tile0 = blockIdx.x * p.per_block;
+  if (tile0 >= n) return;
+  {  // several threads per head share the pieces, then one joins them
+    const long long G = min(p.G, total);
+    const long long s0 = share_of(before, total, G), s1 = share_of(before + n - 1, total, G);
+    const int per = ST / p.Hp, h = threadIdx.x % p.Hp, part = threadIdx.x / p.Hp;
+    float m = -INFINITY, l = 0.f;
+    if (part < per && h < p.H) {
+      for (long long s = s0 + part; s <= s1; s += per) m = fmaxf(m, p.part_m[(s + b) * p.H + h]);
+      if (m != -INFINITY)
+        for (long long s = s0 + part; s <= s1; s += per)
+          l += p.part_l[(s + b) * p.H + h] * exp2f(p.part_m[(s + b) * p.H + h] - m);
+    }
+    m_s[threadIdx.x] = m;
+    l_s[threadIdx.x] = l;
+    __syncthreads();
+    if (threadIdx.x < p.Hp) {
+      for (int k = 1; k < per; ++k) m = fmaxf(m, m_s[threadIdx.x + k * p.Hp]);
+      float sum = 0.f;
+      for (int k = 0; k < per; ++k) {
+        const float mk = m_s[threadIdx.x + k * p.Hp];
+        if (mk != -INFINITY) sum += l_s[threadIdx.x + k * p.Hp] * exp2f(mk - m);
+      }
+      lse_s[threadIdx.x] = m + log2f(sum);
+    }
+    __syncthreads();
+  }
+  const int lane = threadIdx.x & 31;
+  float lse[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) lse[i] = 32 * i + lane < p.H ? lse_s[32 * i + lane] : 0.f;
+  const float4 *S = reinterpret_cast<const float4 *>(p.S) +
+                    ((size_t)b * p.tiles_max + tile0) * (kScoreTileKeys / 4) * p.Hp + lane;
+  float *score = p.score + (size_t)b * p.score_ld;
+  const int rows0 = tile0 * kScoreTileKeys, rows = min(p.per_block * kScoreTileKeys, len - rows0);
+  constexpr int Q = 4;  // quads per warp and step
+  for (int r0 = 4 * Q * (threadIdx.x >> 5); r0 < rows; r0 += 4 * Q * (ST / 32)) {
+    float4 x[Q][3];
+#pragma unroll
+    for (int k = 0; k < Q; ++k)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (r0 + 4 * k < rows && 32 * i + lane < p.H) x[k][i] = __ldcs(S + (size_t)(r0 / 4 + k) * p.Hp + 32 * i);
+#pragma unroll
+    for (int k = 0; k < Q; ++k) {
+      const int r = r0 + 4 * k;
+      float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (r < rows && 32 * i + lane < p.H) {
+          v[0] += fast_exp2(x[k][i].x - lse[i]);
+          v[1] += fast_exp2(x[k][i].y - lse[i]);
+          v[2] += fast_exp2(x[k][i].z - lse[i]);
+          v[3] += fast_exp2(x[k][i].w - lse[i]);
+        }
+      }
+      // sums over the lanes; lane 8k ends up with row r + k
+      const bool up16 = lane & 16, up8 = lane & 8;
+      const float a0 = (up16 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, up16 ? v[0] : v[2], 16);
+      const float a1 = (up16 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, up16 ? v[1] : v[3], 16);
+      float a = (up8 ? a1 : a0) + __shfl_xor_sync(0xffffffffu, up8 ? a0 : a1, 8);
+#pragma unroll
+      for (int o = 4; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+      if ((lane & 7) == 0 && r + lane / 8 < rows) {
+        float *dst = score + rows0 + r + lane / 8;
+        *dst = fmaf(p.decay, *dst, a);
+      }
+    }
+  }
+}
+
+}  // namespace cache_score
+
+int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
+  using namespace cache_score;
+  uint8_t *ws = static_cast<uint8_t *>(a.workspace);
+  const ScoreLayout lay = score_layout(reinterpret_cast<uintptr_t>(ws), a.B, a.L, a.H, a.dc);
+  uint16_t *hi = reinterpret_cast<uint16_t *>(ws + lay.hi), *lo = reinterpret_cast<uint16_t *>(ws + lay.lo);
+  constexpr float kLog2e = 1.4426950408889634f;
+  if (!set_smem_limit_once(reinterpret_cast<const void *>(scores_kernel), (int)smem_bytes(), kSmemScore)) return -1;
+  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e, nullptr, hi, lo, a.status, stream) != 0)
+    return -1;
+  const int group = (int)score_group(a.B, a.L, a.H);
+  for (int b0 = 0; b0 < a.B; b0 += group) {
+    const int nb = a.B - b0 < group ? a.B - b0 : group;
+    CUtensorMap tq, tc;
+    const long long dq[3] = {a.dc, a.H, nb}, sq[2] = {a.dc, (long long)a.H * a.dc};
+    const unsigned bq[3] = {64, HMAX, 1};
+    const long long dcm[3] = {a.dc, a.L, nb}, scm[2] = {a.dc, a.cache_len_max * a.dc};
+    const unsigned bc[3] = {64, KT, 1};
+    if (!make_tmap_bf16(&tq, hi + (size_t)b0 * a.H * a.dc, 3, dq, sq, bq) ||
+        !make_tmap_bf16(&tc, a.C + (size_t)b0 * a.cache_len_max * a.dc, 3, dcm, scm, bc))
+      return -1;
+    Params p;
+    p.H = a.H;
+    p.dc = a.dc;
+    p.Hp = (int)score_heads(a.H);
+    p.tiles_max = score_tiles(a.L);
+    p.batch = ShareBatch{a.lens ? a.lens + b0 : nullptr, nb, a.L, KT};
+    p.lo = lo + (size_t)b0 * a.H * a.dc;
+    p.part_m = reinterpret_cast<float *>(ws + lay.pm);
+    p.part_l = reinterpret_cast<float *>(ws + lay.pl);
+    p.S = reinterpret_cast<float *>(ws + lay.s);
+    p.status = a.status;
+    const long long G = share_count(nb, a.L, KT);
+    scores_kernel<<<(unsigned)G, NUM_THREADS, smem_bytes(), stream>>>(tq, tc, p);
+    SumParams u;
+    u.batch = p.batch;
+    u.G = G;
+    u.tiles_max = p.tiles_max;
+    u.H = p.H;
+    u.Hp = p.Hp;
+    u.part_m = p.part_m;
+    u.part_l = p.part_l;
+    u.S = p.S;
+    u.decay = a.decay;
+    u.score = a.score + (size_t)b0 * a.cache_len_max;
+    u.score_ld = a.cache_len_max;
+    // one tile per block until there are eight blocks per SM (each repeats the join of the pieces' states)
+    const long long per = p.tiles_max * nb / (8 * kShares);
+    u.per_block = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+    sum_kernel<<<dim3((unsigned)((p.tiles_max + u.per_block - 1) / u.per_block), nb), ST, 0, stream>>>(u);
+    if (cudaGetLastError() != cudaSuccess) return -1;
+  }
+  return 0;
+}
+
+}  // namespace gmla

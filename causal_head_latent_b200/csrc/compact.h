@@ -53,4 +53,18 @@ struct Fp4DecodeArgs {
 };
 int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream);
 
+// ---------------------------------------------------------------- accumulated weights
+struct ScoreArgs {
+  const uint16_t *Q, *C;
+  long long cache_len_max;
+  int B, L, H, dc;
+  const int *lens;  // optional device [B], clamped to 0..L
+  const uint16_t *Wk;
+  float scale, decay;
+  float *score;  // [B, cache_len_max]
+  void *workspace;
+  unsigned *status;
+};
+int launch_cache_score(const ScoreArgs &a, cudaStream_t stream);
+
 }  // namespace gmla

@@ -90,4 +90,31 @@ gmla_status gmla_attend_decode_fp4(const gmla_bf16 *Q, const uint8_t *codes, con
   return launch_attend_fp4(a, static_cast<cudaStream_t>(stream)) == 0 ? GMLA_OK : GMLA_ERR_CUDA;
 }
 
+size_t gmla_cache_score_workspace_size(int64_t B, int64_t L, int64_t H, int64_t d_c) {
+  if (B <= 0 || L <= 0 || H <= 0 || d_c <= 0) return 0;
+  return score_layout_bytes(B, L, H, d_c);
+}
+
+gmla_status gmla_cache_score(const gmla_bf16 *Q, const gmla_bf16 *C, int64_t B, int64_t cache_len_max, int64_t L,
+                             const int32_t *lens, int64_t H, int64_t D_h, int64_t d_c, const gmla_bf16 *W_k,
+                             float scale, float decay, float *score, void *workspace, size_t workspace_bytes,
+                             gmla_stream_t stream) {
+  if (!Q || !C || !W_k || !score) return GMLA_ERR_ARG;
+  if (B <= 0 || H <= 0 || D_h <= 0 || d_c <= 0 || L < 1 || cache_len_max < L) return GMLA_ERR_ARG;
+  const void *ptrs[] = {Q, C, W_k, workspace};
+  for (const void *p : ptrs)
+    if (!aligned(p)) return GMLA_ERR_ARG;
+  if (!aligned(score, 4) || !aligned(lens, 4) || !isfinite(decay)) return GMLA_ERR_ARG;
+  if (D_h != 128 || !latent_width_ok(d_c) || H > 96) return GMLA_ERR_UNSUPPORTED;
+  if (B > kMaxBatch || L > 0x7fffff00LL) return GMLA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < gmla_cache_score_workspace_size(B, L, H, d_c)) return GMLA_ERR_WORKSPACE;
+  if (scale <= 0.f) scale = 1.0f / sqrtf((float)D_h);
+  unsigned *st = status_ptr();
+  if (!st) return GMLA_ERR_CUDA;
+  ScoreArgs a{};
+  a.Q = Q; a.C = C; a.cache_len_max = cache_len_max; a.B = (int)B; a.L = (int)L; a.H = (int)H; a.dc = (int)d_c;
+  a.lens = lens; a.Wk = W_k; a.scale = scale; a.decay = decay; a.score = score; a.workspace = workspace; a.status = st;
+  return launch_cache_score(a, static_cast<cudaStream_t>(stream)) == 0 ? GMLA_OK : GMLA_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -16,6 +16,7 @@
 namespace gmla {
 
 constexpr int kFp4TileKeys = 48;     // cached rows per tile of the 4-bit decode
+constexpr int kScoreTileKeys = 128;  // ... and of the accumulated weights
 
 // The tiles of all sequences, laid end to end, are cut into G equal shares, one
 // per CTA, whatever the lengths: CTA i works tiles [share_begin(i), share_begin(i+1)).
@@ -59,6 +60,47 @@ inline Fp4DecodeLayout fp4_decode_layout(uintptr_t base, long long B, long long 
 }
 inline size_t fp4_decode_layout_bytes(long long B, long long L, long long H, long long dc) {
   return (kWsAlign - 16) + fp4_decode_layout(0, B, L, H, dc).end;
+}
+
+// Accumulated weights: the scores of a group of sequences pass through the workspace, as
+// [sequence][tile][key / 4][head, rounded up to 32][key % 4] float32, at most
+// kScoreScratchBytes of them (at least one sequence).
+constexpr long long kScoreScratchBytes = 256ll << 20;
+
+inline long long score_heads(long long H) { return (H + 31) / 32 * 32; }
+inline long long score_tiles(long long L) { return (L + kScoreTileKeys - 1) / kScoreTileKeys; }
+inline long long score_seq_bytes(long long L, long long H) {
+  return score_tiles(L) * kScoreTileKeys * score_heads(H) * 4;
+}
+inline long long score_group(long long B, long long L, long long H) {
+  const long long n = kScoreScratchBytes / score_seq_bytes(L, H);
+  return n < 1 ? 1 : n > B ? B : n;
+}
+
+// q~ as bfloat16 hi and lo [B,H,dc] | m, l float [R,H] of a group | the group's scores.
+struct ScoreLayout {
+  size_t hi, lo, pm, pl, s, end;
+};
+inline ScoreLayout score_layout(uintptr_t base, long long B, long long L, long long H, long long dc) {
+  const long long n = score_group(B, L, H);
+  const size_t R = (size_t)share_records(n, L, kScoreTileKeys);
+  ScoreLayout o;
+  size_t off = ws_round(base) - base;
+  o.hi = off;
+  off += ws_round(2 * (size_t)B * H * dc);
+  o.lo = off;
+  off += ws_round(2 * (size_t)B * H * dc);
+  o.pm = off;
+  off += ws_round(4 * R * H);
+  o.pl = off;
+  off += ws_round(4 * R * H);
+  o.s = off;
+  off += ws_round((size_t)n * score_seq_bytes(L, H));
+  o.end = off;
+  return o;
+}
+inline size_t score_layout_bytes(long long B, long long L, long long H, long long dc) {
+  return (kWsAlign - 16) + score_layout(0, B, L, H, dc).end;
 }
 
 }  // namespace gmla

@@ -158,6 +158,13 @@ __device__ __forceinline__ bool mbar_wait_limit(uint64_t *bar, uint32_t parity, 
   }
 }
 
+// Waits of a whole converged warp; every lane gets the same answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned *status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status)) != 0;
+}
+__device__ __forceinline__ bool warp_wait_relaxed(uint64_t *bar, uint32_t parity, unsigned *status) {
+  return __all_sync(0xffffffffu, mbar_wait_relaxed(bar, parity, status)) != 0;
+}
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
@@ -308,6 +315,16 @@ __device__ __forceinline__ void umma_f16_ss_if(uint32_t issue, uint32_t d_tmem, 
 __device__ __forceinline__ void umma_commit(uint64_t *bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                : "memory");
+}
+
+// A from tensor memory (lane = row, two 16-bit elements per column).
+__device__ __forceinline__ void umma_f16_ts_if(uint32_t issue, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+      : "memory");
 }
 
 __device__ __forceinline__ void umma_commit_if(uint32_t issue, uint64_t *bar) {

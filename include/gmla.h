@@ -35,6 +35,7 @@
  *                            d_c = 512), and back:
  *  gmla_cache_dequantize_fp4   bfloat16 rows of a range of 4-bit rows
  *  gmla_attend_decode_fp4    gmla_attend_decode over 4-bit rows
+ *  gmla_cache_score          attention weight of every cached row, accumulated over steps
  *  gmla_gate_out             the gate and output projection Y = (sigmoid(G) (.) O) W_o^T
  *  gmla_gate_out_heads       its share for a range of heads (head-parallel prefill)
  *  gmla_get_device_status, gmla_selftest_wait_timeout, gmla_status_string,
@@ -497,6 +498,31 @@ GMLA_API gmla_status gmla_attend_decode_fp4(const gmla_bf16 *Q, const uint8_t *c
                                             const gmla_bf16 *G, gmla_bf16 *O, void *workspace,
                                             size_t workspace_bytes, gmla_stream_t stream);
 GMLA_API size_t gmla_attend_decode_fp4_workspace_size(int64_t B, int64_t L, int64_t H, int64_t d_c);
+
+/*
+ * gmla_cache_score -- the attention weight that every cached row gets from one
+ * new query per sequence, summed over the heads and added to a running score:
+ *     score[b, s] = decay * score[b, s] + sum_h a_bhs
+ * with a_bhs the softmax weights of gmla_attend_decode (rows of every head sum
+ * to 1, so a call adds H to the scores of a sequence).  What gmla_cache_evict
+ * goes by.  Float32 throughout: the absorbed query is carried with about 16 bits
+ * (two bfloat16 parts), the cache rows as they are.
+ *
+ *  Q, C, W_k, scale  as gmla_attend_decode
+ *  L, lens  as gmla_attend_decode_fp4 (lens: optional DEVICE int32 array).  Scores of
+ *          rows at or past a sequence's length are left as they were.
+ *  decay   finite; 1 accumulates, less than 1 forgets
+ *  score   float32 [B, cache_len_max], in/out
+ *  workspace >= gmla_cache_score_workspace_size(B, L, H, d_c) bytes, 16-byte
+ *          aligned: the scores of a group of sequences pass through it (256 MB, or
+ *          one sequence's if that is more).  Calls that may overlap on the GPU need one each.
+ * Errors as gmla_attend_decode; GMLA_ERR_ARG also when decay is not finite.
+ */
+GMLA_API gmla_status gmla_cache_score(const gmla_bf16 *Q, const gmla_bf16 *C, int64_t B, int64_t cache_len_max,
+                                      int64_t L, const int32_t *lens, int64_t H, int64_t D_h, int64_t d_c,
+                                      const gmla_bf16 *W_k, float scale, float decay, float *score, void *workspace,
+                                      size_t workspace_bytes, gmla_stream_t stream);
+GMLA_API size_t gmla_cache_score_workspace_size(int64_t B, int64_t L, int64_t H, int64_t d_c);
 
 /* Synchronise `stream`, then read and clear this device's status word.
  * Returns GMLA_OK, GMLA_ERR_TIMEOUT (a bounded wait ran out) or GMLA_ERR_CUDA. */
