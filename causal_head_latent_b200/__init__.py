@@ -25,6 +25,7 @@ __all__ = [
     "gmla_decode_combine", "gmla_attend_decode_noalloc", "gmla_attend_decode_noalloc_max_bytes",
     "gmla_cache_quantize_fp4", "gmla_cache_dequantize_fp4", "gmla_attend_decode_fp4",
     "gmla_attend_decode_fp4_workspace_size", "gmla_cache_score", "gmla_cache_score_workspace_size",
+    "gmla_cache_evict", "gmla_cache_evict_workspace_size",
     "gmla_gate_out", "gmla_gate_out_heads", "gmla_gate_out_workspace_size", "gmla_get_device_status",
     "gmla_selftest_wait_timeout", "gmla_status_string",
     "gmla_version", "STATUS",
@@ -105,6 +106,11 @@ lib.gmla_cache_score.argtypes = [_p, _p, _i64, _i64, _i64, _p, _i64, _i64, _i64,
 lib.gmla_cache_score.restype = _st
 lib.gmla_cache_score_workspace_size.argtypes = [_i64, _i64, _i64, _i64]
 lib.gmla_cache_score_workspace_size.restype = _sz
+lib.gmla_cache_evict.argtypes = [_p, _i64, _p, _p, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i64, _i64, _p, _i64, _i64,
+                                 _i64, _p, _p, _p, _sz, _p]
+lib.gmla_cache_evict.restype = _st
+lib.gmla_cache_evict_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.gmla_cache_evict_workspace_size.restype = _sz
 lib.gmla_get_device_status.argtypes = [_p]
 lib.gmla_get_device_status.restype = _st
 lib.gmla_selftest_wait_timeout.argtypes = [ctypes.c_uint, _p]
@@ -475,6 +481,53 @@ def gmla_cache_score(Q, C, L, W_k, score, num_heads, lens=None, scale=0.0, decay
     code = lib.gmla_cache_score(_ptr(Q), _ptr(C), B, Lmax, int(L), _ptr(lens), H, _head_width(d, H), d_c, _ptr(W_k),
                                 float(scale), float(decay), _ptr(score), wp, wb, _stream(stream))
     return _check(code, "gmla_cache_score") if check else code
+
+
+def gmla_cache_evict_workspace_size(B, L, keep) -> int:
+    return lib.gmla_cache_evict_workspace_size(B, L, keep)
+
+
+def gmla_cache_evict(rows, score, L, keep, index, new_lens, pos=None, lens=None, sink=0, recent=0, dst=None,
+                     dst_score=None, dst_pos=None, workspace=None, stream=None, check=True):
+    """Keep the `keep` best rows of every sequence by score.  rows: one or two tensors [B, cache_len_max, width]
+    (a bfloat16 cache, or codes and scales); score float32 [B, cache_len_max]; pos int32 [B, cache_len_max] or
+    None; dst, dst_score, dst_pos: the same kinds of tensors [B, dst_len_max, ...], or all None for in place;
+    outputs index int32 [B, keep] and new_lens int32 [B] (may be lens); see include/gmla.h."""
+    rows = list(rows)
+    if not 1 <= len(rows) <= 2:
+        raise ValueError("rows must hold one or two tensors")
+    B, Lmax = score.shape
+    _tensor(score, "score", torch.float32, (B, Lmax))
+    for t in rows:
+        _tensor(t, "rows", t.dtype, (B, Lmax, None))
+    if pos is not None:
+        _tensor(pos, "pos", torch.int32, (B, Lmax))
+    if dst is None:
+        if dst_score is not None or dst_pos is not None:
+            raise ValueError("dst_score and dst_pos go with dst")
+        dst, dst_score, dst_pos = rows, score, pos
+    else:
+        dst = list(dst)
+        if len(dst) != len(rows) or dst_score is None or (dst_pos is None) != (pos is None):
+            raise ValueError("dst, dst_score and dst_pos must match rows, score and pos")
+    Dmax = dst_score.shape[1]
+    _tensor(dst_score, "dst_score", torch.float32, (B, Dmax))
+    for t, r in zip(dst, rows):
+        _tensor(t, "dst", r.dtype, (B, Dmax, r.shape[2]))
+    if pos is not None:
+        _tensor(dst_pos, "dst_pos", torch.int32, (B, Dmax))
+    if lens is not None:
+        _tensor(lens, "lens", torch.int32, (B,))
+    _tensor(index, "index", torch.int32, (B, int(keep)))
+    _tensor(new_lens, "new_lens", torch.int32, (B,))
+    r1, d1 = (rows[1], dst[1]) if len(rows) == 2 else (None, None)
+    wp, wb = _ws(workspace)
+    code = lib.gmla_cache_evict(_ptr(rows[0]), rows[0].shape[2] * rows[0].element_size(), _ptr(dst[0]), _ptr(r1),
+                                0 if r1 is None else r1.shape[2] * r1.element_size(), _ptr(d1), _ptr(score),
+                                _ptr(dst_score), _ptr(pos), _ptr(dst_pos), B, Lmax, Dmax, int(L), _ptr(lens),
+                                int(keep), int(sink), int(recent), _ptr(new_lens), _ptr(index), wp, wb,
+                                _stream(stream))
+    return _check(code, "gmla_cache_evict") if check else code
 
 
 def _head_width(d, H):

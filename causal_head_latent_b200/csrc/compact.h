@@ -67,4 +67,26 @@ struct ScoreArgs {
 };
 int launch_cache_score(const ScoreArgs &a, cudaStream_t stream);
 
+// ---------------------------------------------------------------- eviction
+struct EvictRows {
+  const void *src;  // [B, cache_len_max] rows of `bytes` bytes; null: none
+  void *dst;        // [B, dst_len_max]
+  int bytes;
+  bool wide;  // rows in 16-byte words (else 4)
+};
+struct EvictArgs {
+  EvictRows rows[2];
+  const float *score;
+  const int *pos;
+  float *dst_score;
+  int *dst_pos;
+  bool in_place;
+  long long cache_len_max, dst_len_max;
+  int B, L, keep, sink, recent;
+  const int *lens;
+  int *new_lens, *index;
+  void *workspace;
+};
+int launch_cache_evict(const EvictArgs &a, cudaStream_t stream);
+
 }  // namespace gmla

@@ -117,4 +117,51 @@ gmla_status gmla_cache_score(const gmla_bf16 *Q, const gmla_bf16 *C, int64_t B, 
   return launch_cache_score(a, static_cast<cudaStream_t>(stream)) == 0 ? GMLA_OK : GMLA_ERR_CUDA;
 }
 
+size_t gmla_cache_evict_workspace_size(int64_t B, int64_t L, int64_t keep) {
+  if (B <= 0 || L <= 0 || keep <= 0) return 0;
+  return evict_layout_bytes(B, keep);
+}
+
+gmla_status gmla_cache_evict(const void *rows0, int64_t row_bytes0, void *dst0, const void *rows1, int64_t row_bytes1,
+                             void *dst1, const float *score, float *dst_score, const int32_t *pos, int32_t *dst_pos,
+                             int64_t B, int64_t cache_len_max, int64_t dst_len_max, int64_t L, const int32_t *lens,
+                             int64_t keep, int64_t sink, int64_t recent, int32_t *new_lens, int32_t *index,
+                             void *workspace, size_t workspace_bytes, gmla_stream_t stream) {
+  if (!rows0 || !dst0 || !score || !dst_score || !new_lens || !index) return GMLA_ERR_ARG;
+  if (!rows1 != !dst1 || !pos != !dst_pos) return GMLA_ERR_ARG;
+  if (B <= 0 || L < 1 || cache_len_max < L || dst_len_max < 1) return GMLA_ERR_ARG;
+  if (keep < 1 || sink < 0 || recent < 0 || sink > keep || recent > keep - sink) return GMLA_ERR_ARG;
+  const int64_t bytes[2] = {row_bytes0, rows1 ? row_bytes1 : 4};
+  for (int64_t n : bytes)
+    if (n < 4 || n % 4 || n > 65536) return GMLA_ERR_ARG;
+  const void *wide[] = {rows0, dst0, rows1, dst1, workspace}, *narrow[] = {score, dst_score, pos, dst_pos, lens, new_lens, index};
+  for (const void *p : wide)
+    if (!aligned(p)) return GMLA_ERR_ARG;
+  for (const void *p : narrow)
+    if (!aligned(p, 4)) return GMLA_ERR_ARG;
+  if (B > kMaxBatch || L >= 0x7fffff00LL || keep >= 0x7fffff00LL || cache_len_max > (int64_t(1) << 40) ||
+      dst_len_max > (int64_t(1) << 40))
+    return GMLA_ERR_UNSUPPORTED;
+  const struct { const void *src; void *dst; int64_t bytes; } arrays[] = {
+      {rows0, dst0, bytes[0]}, {rows1, dst1, bytes[1]}, {score, dst_score, 4}, {pos, dst_pos, 4}};
+  const bool in_place = rows0 == dst0;
+  for (const auto &a : arrays) {
+    if (!a.src) continue;
+    if ((a.src == a.dst) != in_place) return GMLA_ERR_ARG;
+    const char *s = static_cast<const char *>(a.src), *d = static_cast<const char *>(a.dst);
+    if (!in_place && d < s + B * cache_len_max * a.bytes && s < d + B * dst_len_max * a.bytes) return GMLA_ERR_ARG;
+  }
+  if (in_place ? dst_len_max != cache_len_max : dst_len_max < (keep < L ? keep : L)) return GMLA_ERR_ARG;
+  if (!workspace || workspace_bytes < gmla_cache_evict_workspace_size(B, L, keep)) return GMLA_ERR_WORKSPACE;
+  if (!status_ptr()) return GMLA_ERR_CUDA;
+  EvictArgs a{};
+  a.rows[0] = EvictRows{rows0, dst0, (int)bytes[0], bytes[0] % 16 == 0};
+  if (rows1) a.rows[1] = EvictRows{rows1, dst1, (int)bytes[1], bytes[1] % 16 == 0};
+  a.score = score; a.dst_score = dst_score; a.pos = pos; a.dst_pos = dst_pos; a.in_place = in_place;
+  a.cache_len_max = cache_len_max; a.dst_len_max = dst_len_max;
+  a.B = (int)B; a.L = (int)L; a.keep = (int)keep; a.sink = (int)sink; a.recent = (int)recent;
+  a.lens = lens; a.new_lens = new_lens; a.index = index; a.workspace = workspace;
+  return launch_cache_evict(a, static_cast<cudaStream_t>(stream)) == 0 ? GMLA_OK : GMLA_ERR_CUDA;
+}
+
 }  // extern "C"

@@ -103,4 +103,7 @@ inline size_t score_layout_bytes(long long B, long long L, long long H, long lon
   return (kWsAlign - 16) + score_layout(0, B, L, H, dc).end;
 }
 
+// Eviction: the rows that fill holes, int32 [B, keep].
+inline size_t evict_layout_bytes(long long B, long long keep) { return (kWsAlign - 16) + ws_round(4 * (size_t)B * keep); }
+
 }  // namespace gmla

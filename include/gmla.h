@@ -36,6 +36,7 @@
  *  gmla_cache_dequantize_fp4   bfloat16 rows of a range of 4-bit rows
  *  gmla_attend_decode_fp4    gmla_attend_decode over 4-bit rows
  *  gmla_cache_score          attention weight of every cached row, accumulated over steps
+ *  gmla_cache_evict          the best rows of a cache by that weight, the rest dropped
  *  gmla_gate_out             the gate and output projection Y = (sigmoid(G) (.) O) W_o^T
  *  gmla_gate_out_heads       its share for a range of heads (head-parallel prefill)
  *  gmla_get_device_status, gmla_selftest_wait_timeout, gmla_status_string,
@@ -523,6 +524,50 @@ GMLA_API gmla_status gmla_cache_score(const gmla_bf16 *Q, const gmla_bf16 *C, in
                                       const gmla_bf16 *W_k, float scale, float decay, float *score, void *workspace,
                                       size_t workspace_bytes, gmla_stream_t stream);
 GMLA_API size_t gmla_cache_score_workspace_size(int64_t B, int64_t L, int64_t H, int64_t d_c);
+
+/*
+ * gmla_cache_evict -- keep the `keep` best cached rows of every sequence by
+ * accumulated attention weight (gmla_cache_score) and drop the others.
+ *
+ * Of the rows 0..len-1 of a sequence (len = L or lens[b]) n = min(keep, len)
+ * stay: protected rows first, then by score, highest first; ties go to the lowest row,
+ * and a NaN score is below every number.  A row is protected when its position is
+ * below `sink` or among the `recent` newest (above newest - recent, newest the
+ * largest position among the rows).  The layer has no positional encoding, so
+ * the order of cached rows carries no meaning and rows are not shifted: kept rows
+ * below n stay where they are, and the places below n that are not kept, ascending,
+ * take the kept rows at or past n, ascending.
+ *
+ *  rows0, rows1  one or two arrays [B, cache_len_max] of rows of row_bytes0 and
+ *          row_bytes1 bytes (multiples of 4, at most 65536; rows1 may be NULL): a bfloat16
+ *          cache, or the codes and scales of a 4-bit one
+ *  dst0, dst1  where the kept rows go, [B, dst_len_max].  In place when every
+ *          destination is its source (then dst_len_max == cache_len_max): only
+ *          rows that change place are written.  Otherwise none may overlap its
+ *          source, min(keep, L) <= dst_len_max, and rows 0..n-1 are written.
+ *          Rows at or past n of a destination are left as they were.
+ *  score   float32 [B, cache_len_max], moved with the rows into dst_score
+ *  pos     optional int32 [B, cache_len_max]: the token position of each row,
+ *          moved into dst_pos.  NULL: a row's position is its index, which
+ *          holds until a first eviction in place.
+ *  L, lens  as gmla_attend_decode_fp4 (lens: optional DEVICE int32 array)
+ *  keep >= 1, sink, recent >= 0, sink + recent <= keep
+ *  new_lens  int32 [B] output: n.  May be lens.
+ *  index   int32 [B, keep] output: the row that row j came from, -1 for j >= n
+ *  workspace >= gmla_cache_evict_workspace_size(B, L, keep) bytes, 16-byte
+ *          aligned.  Calls that may overlap on the GPU need one each.
+ * Every pointer but scores', positions', lengths' and index's (4 bytes) is 16-byte aligned.
+ * Errors: GMLA_ERR_ARG for null, misaligned or overlapping pointers and sizes
+ * outside these bounds; GMLA_ERR_UNSUPPORTED for B > 65535 or lengths of 2^31 - 256 or
+ * more; GMLA_ERR_WORKSPACE.
+ */
+GMLA_API gmla_status gmla_cache_evict(const void *rows0, int64_t row_bytes0, void *dst0, const void *rows1,
+                                      int64_t row_bytes1, void *dst1, const float *score, float *dst_score,
+                                      const int32_t *pos, int32_t *dst_pos, int64_t B, int64_t cache_len_max,
+                                      int64_t dst_len_max, int64_t L, const int32_t *lens, int64_t keep, int64_t sink,
+                                      int64_t recent, int32_t *new_lens, int32_t *index, void *workspace,
+                                      size_t workspace_bytes, gmla_stream_t stream);
+GMLA_API size_t gmla_cache_evict_workspace_size(int64_t B, int64_t L, int64_t keep);
 
 /* Synchronise `stream`, then read and clear this device's status word.
  * Returns GMLA_OK, GMLA_ERR_TIMEOUT (a bounded wait ran out) or GMLA_ERR_CUDA. */
