@@ -386,25 +386,36 @@ def gmla_decode_combine(lse, ctx, W_v, O, G=None, stream=None, check=True):
     return _check(code, "gmla_decode_combine") if check else code
 
 
-def _tensor(t, name, dtype, shape):
-    """A contiguous tensor of this type and shape (None in `shape`: any extent) on the current device."""
+def _tensor(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor of this type and shape on device `dev` (None for None).  The checks of
+    a call are most of its host time, so the usual case takes four comparisons."""
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {str(dtype).replace('torch.', '')}")
-    if t.dim() != len(shape) or any(w is not None and int(n) != int(w) for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple('any' if w is None else w for w in shape)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} must live on the current CUDA device")
-    return t
+    raise ValueError(f"{name} must live on the current CUDA device")
 
 
-def _fp4_rows(codes, scales):
-    """(B, cache_len_max, d_c) of a 4-bit cache."""
-    _tensor(codes, "codes", torch.uint8, (None, None, None))
-    B, Lmax, half = codes.shape
-    _tensor(scales, "scales", torch.uint8, (B, Lmax, half // 8))
-    return B, Lmax, 2 * half
+def _shape(t, name, dims):
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, has {t.dim()}")
+    return t.shape
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _head_width(d, H):
+    if H < 1 or d % H:
+        raise ValueError(f"num_heads {H} does not divide the model width {d}")
+    return d // H
 
 
 def gmla_cache_quantize_fp4(C, codes, scales, src_row0=0, rows=None, row0=0, row_of=None, cache_scale=1.0, stream=None,
@@ -412,13 +423,15 @@ def gmla_cache_quantize_fp4(C, codes, scales, src_row0=0, rows=None, row0=0, row
     """Rows src_row0 .. src_row0+rows-1 of C [B, src_len_max, d_c] (all from src_row0 on when rows is None)
     into rows row0 .. (or row_of[b] .., an int32 tensor on the device) of codes [B, cache_len_max, d_c/2] and
     scales [B, cache_len_max, d_c/16], both uint8 (see include/gmla.h)."""
-    B, Lmax, d_c = _fp4_rows(codes, scales)
-    _tensor(C, "C", torch.bfloat16, (B, None, d_c))
-    if row_of is not None:
-        _tensor(row_of, "row_of", torch.int32, (B,))
-    n = C.shape[1] - int(src_row0) if rows is None else int(rows)
-    code = lib.gmla_cache_quantize_fp4(_ptr(C), B, C.shape[1], int(src_row0), n, d_c, float(cache_scale), _ptr(codes),
-                                       _ptr(scales), Lmax, int(row0), _ptr(row_of), _stream(stream))
+    dev = torch.cuda.current_device()
+    B, n_src, d_c = _shape(C, "C", 3)
+    Lmax = _shape(codes, "codes", 3)[1]
+    n = n_src - src_row0 if rows is None else rows
+    code = lib.gmla_cache_quantize_fp4(
+        _tensor(C, "C", torch.bfloat16, (B, n_src, d_c), dev), B, n_src, src_row0, n, d_c, cache_scale,
+        _tensor(codes, "codes", torch.uint8, (B, Lmax, d_c // 2), dev),
+        _tensor(scales, "scales", torch.uint8, (B, Lmax, d_c // 16), dev), Lmax, row0,
+        _tensor(row_of, "row_of", torch.int32, (B,), dev), _raw_stream(stream, dev))
     return _check(code, "gmla_cache_quantize_fp4") if check else code
 
 
@@ -426,11 +439,14 @@ def gmla_cache_dequantize_fp4(codes, scales, C, row0=0, rows=None, dst_row0=0, c
                               check=True):
     """Rows row0 .. row0+rows-1 (all from row0 on when rows is None) of a 4-bit cache as bfloat16 rows
     dst_row0 .. of C [B, dst_len_max, d_c]."""
-    B, Lmax, d_c = _fp4_rows(codes, scales)
-    _tensor(C, "C", torch.bfloat16, (B, None, d_c))
-    n = Lmax - int(row0) if rows is None else int(rows)
-    code = lib.gmla_cache_dequantize_fp4(_ptr(codes), _ptr(scales), B, Lmax, int(row0), n, d_c, float(cache_scale),
-                                         _ptr(C), C.shape[1], int(dst_row0), _stream(stream))
+    dev = torch.cuda.current_device()
+    B, n_dst, d_c = _shape(C, "C", 3)
+    Lmax = _shape(codes, "codes", 3)[1]
+    n = Lmax - row0 if rows is None else rows
+    code = lib.gmla_cache_dequantize_fp4(
+        _tensor(codes, "codes", torch.uint8, (B, Lmax, d_c // 2), dev),
+        _tensor(scales, "scales", torch.uint8, (B, Lmax, d_c // 16), dev), B, Lmax, row0, n, d_c, cache_scale,
+        _tensor(C, "C", torch.bfloat16, (B, n_dst, d_c), dev), n_dst, dst_row0, _raw_stream(stream, dev))
     return _check(code, "gmla_cache_dequantize_fp4") if check else code
 
 
@@ -442,20 +458,16 @@ def gmla_attend_decode_fp4(Q, codes, scales, L, W_k, W_v, O, num_heads, cache_sc
                            workspace=None, stream=None, check=True):
     """Decode over a 4-bit cache: Q, O, G [B, H*D]; rows 0..L-1 visible, or 0..lens[b]-1 with lens an int32
     tensor of B lengths on the device (at most L)."""
-    B, Lmax, d_c = _fp4_rows(codes, scales)
-    H = int(num_heads)
-    _tensor(Q, "Q", torch.bfloat16, (B, None))
-    d = Q.shape[1]
-    for n, t, shape in (("W_k", W_k, (d, d_c)), ("W_v", W_v, (d, d_c)), ("O", O, (B, d))):
-        _tensor(t, n, torch.bfloat16, shape)
-    if G is not None:
-        _tensor(G, "G", torch.bfloat16, (B, d))
-    if lens is not None:
-        _tensor(lens, "lens", torch.int32, (B,))
+    dev = torch.cuda.current_device()
+    B, Lmax, half = _shape(codes, "codes", 3)
+    d, d_c, bf16 = _shape(Q, "Q", 2)[1], 2 * half, torch.bfloat16
     wp, wb = _ws(workspace)
-    code = lib.gmla_attend_decode_fp4(_ptr(Q), _ptr(codes), _ptr(scales), float(cache_scale), B, Lmax, int(L),
-                                      _ptr(lens), H, _head_width(d, H), d_c, _ptr(W_k), _ptr(W_v), float(scale),
-                                      _ptr(G), _ptr(O), wp, wb, _stream(stream))
+    code = lib.gmla_attend_decode_fp4(
+        _tensor(Q, "Q", bf16, (B, d), dev), _tensor(codes, "codes", torch.uint8, (B, Lmax, half), dev),
+        _tensor(scales, "scales", torch.uint8, (B, Lmax, half // 8), dev), cache_scale, B, Lmax, L,
+        _tensor(lens, "lens", torch.int32, (B,), dev), num_heads, _head_width(d, num_heads), d_c,
+        _tensor(W_k, "W_k", bf16, (d, d_c), dev), _tensor(W_v, "W_v", bf16, (d, d_c), dev), scale,
+        _tensor(G, "G", bf16, (B, d), dev), _tensor(O, "O", bf16, (B, d), dev), wp, wb, _raw_stream(stream, dev))
     return _check(code, "gmla_attend_decode_fp4") if check else code
 
 
@@ -468,18 +480,15 @@ def gmla_cache_score(Q, C, L, W_k, score, num_heads, lens=None, scale=0.0, decay
     """score [B, cache_len_max] float32 = decay * score + the attention weight of every visible row, summed over
     heads: Q [B, H*D]; C [B, cache_len_max, d_c]; rows 0..L-1 visible, or 0..lens[b]-1 with lens an int32 tensor of
     B lengths on the device (at most L)."""
-    _tensor(C, "C", torch.bfloat16, (None, None, None))
-    B, Lmax, d_c = C.shape
-    H = int(num_heads)
-    _tensor(Q, "Q", torch.bfloat16, (B, None))
-    d = Q.shape[1]
-    _tensor(W_k, "W_k", torch.bfloat16, (d, d_c))
-    _tensor(score, "score", torch.float32, (B, Lmax))
-    if lens is not None:
-        _tensor(lens, "lens", torch.int32, (B,))
+    dev = torch.cuda.current_device()
+    B, Lmax, d_c = _shape(C, "C", 3)
+    d, bf16 = _shape(Q, "Q", 2)[1], torch.bfloat16
     wp, wb = _ws(workspace)
-    code = lib.gmla_cache_score(_ptr(Q), _ptr(C), B, Lmax, int(L), _ptr(lens), H, _head_width(d, H), d_c, _ptr(W_k),
-                                float(scale), float(decay), _ptr(score), wp, wb, _stream(stream))
+    code = lib.gmla_cache_score(
+        _tensor(Q, "Q", bf16, (B, d), dev), _tensor(C, "C", bf16, (B, Lmax, d_c), dev), B, Lmax, L,
+        _tensor(lens, "lens", torch.int32, (B,), dev), num_heads, _head_width(d, num_heads), d_c,
+        _tensor(W_k, "W_k", bf16, (d, d_c), dev), scale, decay,
+        _tensor(score, "score", torch.float32, (B, Lmax), dev), wp, wb, _raw_stream(stream, dev))
     return _check(code, "gmla_cache_score") if check else code
 
 
@@ -493,47 +502,33 @@ def gmla_cache_evict(rows, score, L, keep, index, new_lens, pos=None, lens=None,
     (a bfloat16 cache, or codes and scales); score float32 [B, cache_len_max]; pos int32 [B, cache_len_max] or
     None; dst, dst_score, dst_pos: the same kinds of tensors [B, dst_len_max, ...], or all None for in place;
     outputs index int32 [B, keep] and new_lens int32 [B] (may be lens); see include/gmla.h."""
-    rows = list(rows)
+    dev = torch.cuda.current_device()
+    B, Lmax = _shape(score, "score", 2)
     if not 1 <= len(rows) <= 2:
         raise ValueError("rows must hold one or two tensors")
-    B, Lmax = score.shape
-    _tensor(score, "score", torch.float32, (B, Lmax))
-    for t in rows:
-        _tensor(t, "rows", t.dtype, (B, Lmax, None))
-    if pos is not None:
-        _tensor(pos, "pos", torch.int32, (B, Lmax))
     if dst is None:
         if dst_score is not None or dst_pos is not None:
             raise ValueError("dst_score and dst_pos go with dst")
         dst, dst_score, dst_pos = rows, score, pos
-    else:
-        dst = list(dst)
-        if len(dst) != len(rows) or dst_score is None or (dst_pos is None) != (pos is None):
-            raise ValueError("dst, dst_score and dst_pos must match rows, score and pos")
-    Dmax = dst_score.shape[1]
-    _tensor(dst_score, "dst_score", torch.float32, (B, Dmax))
-    for t, r in zip(dst, rows):
-        _tensor(t, "dst", r.dtype, (B, Dmax, r.shape[2]))
-    if pos is not None:
-        _tensor(dst_pos, "dst_pos", torch.int32, (B, Dmax))
-    if lens is not None:
-        _tensor(lens, "lens", torch.int32, (B,))
-    _tensor(index, "index", torch.int32, (B, int(keep)))
-    _tensor(new_lens, "new_lens", torch.int32, (B,))
-    r1, d1 = (rows[1], dst[1]) if len(rows) == 2 else (None, None)
+    elif len(dst) != len(rows) or dst_score is None or (dst_pos is None) != (pos is None):
+        raise ValueError("dst, dst_score and dst_pos must match rows, score and pos")
+    Dmax = _shape(dst_score, "dst_score", 2)[1]
+    arrays = []
+    for r, t in zip(rows, dst):
+        w = _shape(r, "rows", 3)[2]
+        arrays += [_tensor(r, "rows", r.dtype, (B, Lmax, w), dev), w * r.element_size(),
+                   _tensor(t, "dst", r.dtype, (B, Dmax, w), dev)]
+    if len(rows) == 1:
+        arrays += [None, 0, None]
     wp, wb = _ws(workspace)
-    code = lib.gmla_cache_evict(_ptr(rows[0]), rows[0].shape[2] * rows[0].element_size(), _ptr(dst[0]), _ptr(r1),
-                                0 if r1 is None else r1.shape[2] * r1.element_size(), _ptr(d1), _ptr(score),
-                                _ptr(dst_score), _ptr(pos), _ptr(dst_pos), B, Lmax, Dmax, int(L), _ptr(lens),
-                                int(keep), int(sink), int(recent), _ptr(new_lens), _ptr(index), wp, wb,
-                                _stream(stream))
+    code = lib.gmla_cache_evict(
+        *arrays, _tensor(score, "score", torch.float32, (B, Lmax), dev),
+        _tensor(dst_score, "dst_score", torch.float32, (B, Dmax), dev), _tensor(pos, "pos", torch.int32, (B, Lmax), dev),
+        _tensor(dst_pos, "dst_pos", torch.int32, (B, Dmax), dev), B, Lmax, Dmax, L,
+        _tensor(lens, "lens", torch.int32, (B,), dev), keep, sink, recent,
+        _tensor(new_lens, "new_lens", torch.int32, (B,), dev), _tensor(index, "index", torch.int32, (B, keep), dev),
+        wp, wb, _raw_stream(stream, dev))
     return _check(code, "gmla_cache_evict") if check else code
-
-
-def _head_width(d, H):
-    if H < 1 or d % H:
-        raise ValueError(f"num_heads {H} does not divide the model width {d}")
-    return d // H
 
 
 def gmla_gate_out_workspace_size(M, d_model) -> int:
