@@ -3,17 +3,20 @@
 // Store.  For a group x of 16 channels (x already divided by the power of two
 // cache_scale, so still with bfloat16's 8 significant bits):
 //   s = e4m3(max(min(max|x|, 2688) / 6, 2^-9)),   e_i = e2m1(x_i / s),
-// both rounded to nearest, ties to even.  x_i / s is evaluated as x_i times the
-// float32 reciprocal of s and then rounded to 16 significant bits: a half-way
-// point m between two codes gives m*s with at most 7 bits, so an x_i other than
-// m*s differs from it by 2^-8 relative or more, far outside both roundings, and
-// an x_i equal to m*s lands on m exactly and takes the even code.  The codes are
-// therefore those of the exact quotient.
+// both rounded to nearest, ties to even.  The quotients are products with a float32
+// reciprocal, rounded to 16 significant bits: a half-way point m between two codes gives
+// m*s with at most 7 bits (and 6 m with 8 between two scales), so an x_i other than m*s
+// differs from it by 2^-8 relative or more, far outside both roundings, and an x_i equal
+// to m*s lands on m exactly and takes the even code.  The codes are therefore those of the
+// exact quotient.
 //
-// Both directions are bound by HBM: 2 bytes in and 9/16 byte out per value (or
-// the reverse), a few conversions per value.  One thread holds 8 channels: a
-// warp's loads and stores are then whole 128-byte lines, and a group's maximum
-// is one shuffle between two lanes.  Four vectors per thread in flight.
+// Both directions are bound by HBM: 2 bytes in and 9/16 byte out per value (or the
+// reverse).  One thread holds 8 channels: a warp's loads and stores are then whole
+// 128-byte lines, and a group's maximum is one shuffle between two lanes.  Four vectors per
+// thread in flight.  Storing costs about nine instructions a value, so they are counted:
+// maxima and the NaN test on packed bfloat16, approximate reciprocals (the rounding to 16
+// bits takes their error too), no clamps but the conversions' own.
+#include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 #include "internal.h"
@@ -27,15 +30,30 @@ namespace cache_fp4 {
 constexpr int THREADS = 256;
 constexpr int UNROLL = 4;
 
-// 8 channels of vector v of a sequence: row v / per_row, channels 8 * (v % per_row) ..
+// 8 channels of vector v of a sequence: row t = v / per_row, channels 8 * c8 ..  per_row is
+// a multiple of 8; `magic` is ceil(2^32 / (per_row / 8)), exact for v / 8 < 2^28 (0: per_row is 8).
 struct RowIndex {
   unsigned t, c8;
 };
-__device__ __forceinline__ RowIndex row_index(unsigned v, unsigned per_row) {
+__device__ __forceinline__ RowIndex row_index(unsigned v, unsigned per_row, unsigned magic) {
   RowIndex r;
-  r.t = v / per_row;
+  r.t = magic ? __umulhi(v >> 3, magic) : v >> 3;
   r.c8 = v - r.t * per_row;
   return r;
+}
+static unsigned row_magic(int dc) {
+  const unsigned d = (unsigned)dc / 64;
+  return d == 1 ? 0u : (unsigned)(((1ull << 32) + d - 1) / d);
+}
+
+// x rounded to 16 significant bits.
+__device__ __forceinline__ float round16(float x) {
+  return __uint_as_float((__float_as_uint(x) + 0x80u) & 0xffffff00u);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __global__ void __launch_bounds__(THREADS) quantize_kernel(const Fp4StoreArgs p) {
@@ -49,7 +67,7 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Fp4StoreArgs p)
   for (int k = 0; k < UNROLL; ++k) {
     const unsigned v = v0 + k * THREADS;
     if (v < n) {
-      at[k] = row_index(v, per_row);
+      at[k] = row_index(v, per_row, p.magic);
       ld[k] = __ldcs(reinterpret_cast<const uint4 *>(
           p.C + ((b * p.src_len_max + p.src_row0 + at[k].t) * p.dc + 8 * at[k].c8)));
     } else {
@@ -58,27 +76,25 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const Fp4StoreArgs p)
   }
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k) {
-    const uint32_t w[4] = {ld[k].x, ld[k].y, ld[k].z, ld[k].w};
-    float x[8], top = 0.f;
+    uint32_t w[4] = {ld[k].x, ld[k].y, ld[k].z, ld[k].w};
+    __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16) * p.inv_cache_scale;
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u) * p.inv_cache_scale;
+      const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
+      w[i] &= __heq2_mask(v, v);  // a NaN is held as 0
+      const uint32_t a = w[i] & 0x7fff7fffu;
+      top2 = __hmax2(top2, *reinterpret_cast<const __nv_bfloat162 *>(&a));
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = x[i] == x[i] ? x[i] : 0.f;  // a NaN is held as 0
-      top = fmaxf(top, fabsf(x[i]));
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    const float want = fmaxf(__fdiv_rn(fminf(top, kFp4Max * kFp4ScaleMax), kFp4Max), kFp4ScaleMin);
+    float top = fmaxf(__low2float(top2), __high2float(top2));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1)) * p.inv_cache_scale;
+    const float want = fmaxf(round16(fminf(top, kFp4Max * kFp4ScaleMax) * (1.f / kFp4Max)), kFp4ScaleMin);
     const __nv_fp8_storage_t sb = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
-    const __half2 sh = e4m3x2_to_f16((uint16_t)sb);
-    const float inv = __frcp_rn(__low2float(sh));
+    const float inv = rcp_approx(__low2float(e4m3x2_to_f16((uint16_t)sb)));
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t = fminf(fmaxf(x[i] * inv, -8.f), 8.f);
-      x[i] = __uint_as_float((__float_as_uint(t) + 0x80u) & 0xffffff00u);
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = round16(__uint_as_float(w[i] << 16) * p.inv_cache_scale * inv);
+      x[2 * i + 1] = round16(__uint_as_float(w[i] & 0xffff0000u) * p.inv_cache_scale * inv);
     }
     uint32_t code = f32x8_to_fp4(x);
     // a magnitude that rounds to zero is held as +0
@@ -108,7 +124,7 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Fp4LoadArgs p
   for (int k = 0; k < UNROLL; ++k) {
     const unsigned v = v0 + k * THREADS;
     if (v < n) {
-      at[k] = row_index(v, per_row);
+      at[k] = row_index(v, per_row, p.magic);
       const long long row = b * p.cache_len_max + p.row0 + at[k].t;
       code[k] = __ldcs(reinterpret_cast<const uint32_t *>(p.codes + row * (p.dc / 2) + 4 * at[k].c8));
       sb[k] = p.scales[row * (p.dc / kFp4Group) + at[k].c8 / 2];
@@ -140,12 +156,16 @@ static dim3 grid_of(long long B, long long rows, int dc) {
 }  // namespace cache_fp4
 
 int launch_fp4_store(const Fp4StoreArgs &a, cudaStream_t stream) {
-  cache_fp4::quantize_kernel<<<cache_fp4::grid_of(a.B, a.rows, a.dc), cache_fp4::THREADS, 0, stream>>>(a);
+  Fp4StoreArgs p = a;
+  p.magic = cache_fp4::row_magic(a.dc);
+  cache_fp4::quantize_kernel<<<cache_fp4::grid_of(a.B, a.rows, a.dc), cache_fp4::THREADS, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 int launch_fp4_load(const Fp4LoadArgs &a, cudaStream_t stream) {
-  cache_fp4::dequantize_kernel<<<cache_fp4::grid_of(a.B, a.rows, a.dc), cache_fp4::THREADS, 0, stream>>>(a);
+  Fp4LoadArgs p = a;
+  p.magic = cache_fp4::row_magic(a.dc);
+  cache_fp4::dequantize_kernel<<<cache_fp4::grid_of(a.B, a.rows, a.dc), cache_fp4::THREADS, 0, stream>>>(p);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
