@@ -13,11 +13,11 @@
 // Both directions are bound by HBM: 2 bytes in and 9/16 byte out per value (or the
 // reverse).  One thread holds 8 channels: a warp's loads and stores are then whole
 // 128-byte lines, and a group's maximum is one shuffle between two lanes.  Four vectors per
-// thread in flight.  Storing costs about nine instructions a value, so they are counted:
-// maxima and the NaN test on packed bfloat16, approximate reciprocals (the rounding to 16
-// bits takes their error too), no clamps but the conversions' own.
+// thread in flight, the same channels of rows a block's height apart.  Storing is bound by
+// instructions before memory, so they are counted: maxima (NaN included) on packed
+// bfloat16, approximate reciprocals (the rounding takes their error too), product and
+// rounding as a packed fma and add, no clamps but the conversions' own.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "internal.h"
 #include "compact.h"
@@ -27,24 +27,8 @@
 namespace gmla {
 namespace cache_fp4 {
 
-constexpr int THREADS = 256;
+constexpr int MAX_THREADS = 256;
 constexpr int UNROLL = 4;
-
-// 8 channels of vector v of a sequence: row t = v / per_row, channels 8 * c8 ..  per_row is
-// a multiple of 8; `magic` is ceil(2^32 / (per_row / 8)), exact for v / 8 < 2^28 (0: per_row is 8).
-struct RowIndex {
-  unsigned t, c8;
-};
-__device__ __forceinline__ RowIndex row_index(unsigned v, unsigned per_row, unsigned magic) {
-  RowIndex r;
-  r.t = magic ? __umulhi(v >> 3, magic) : v >> 3;
-  r.c8 = v - r.t * per_row;
-  return r;
-}
-static unsigned row_magic(int dc) {
-  const unsigned d = (unsigned)dc / 64;
-  return d == 1 ? 0u : (unsigned)(((1ull << 32) + d - 1) / d);
-}
 
 // x rounded to 16 significant bits.
 __device__ __forceinline__ float round16(float x) {
@@ -55,84 +39,93 @@ __device__ __forceinline__ float rcp_approx(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+  return r;
+}
+// (a, b) * s + c, then - c: both products rounded to a multiple of c's last bit.
+__device__ __forceinline__ void scale_round2(float &a, float &b, float s, float c) {
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\tmov.b64 z, {%3, %3};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 z, {%4, %4};\n\tadd.rn.f32x2 x, x, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "+f"(a), "+f"(b)
+      : "f"(s), "f"(c), "f"(-c));
+}
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
 
-__global__ void __launch_bounds__(THREADS) quantize_kernel(const Fp4StoreArgs p) {
-  const unsigned per_row = p.dc / 8;
-  const unsigned n = (unsigned)p.rows * per_row;  // a multiple of 8: the lanes of a pair are in or out together
-  const unsigned v0 = blockIdx.x * (THREADS * UNROLL) + threadIdx.x;
+// A block covers blockDim.x / (dc/8) whole rows at a time, UNROLL times: a thread keeps its
+// channels 8 * c8 .. and steps by that many rows.
+__global__ void __launch_bounds__(MAX_THREADS) quantize_kernel(const Fp4StoreArgs p) {
+  const int per_row = p.dc / 8, step = blockDim.x / per_row;
+  const int c8 = threadIdx.x % per_row, t0 = blockIdx.x * (step * UNROLL) + threadIdx.x / per_row;
   const long long b = blockIdx.y;
+  const long long row0 = p.row_of ? (long long)p.row_of[b] : p.row0;
+  // rows that would land outside the cache are dropped: t in [first, last)
+  const int first = (int)max(0ll, min(-row0, p.rows)), last = (int)max(0ll, min(p.rows, p.cache_len_max - row0));
+  const uint16_t *src = p.C + ((b * p.src_len_max + p.src_row0 + t0) * p.dc + 8 * c8);
   uint4 ld[UNROLL];
-  RowIndex at[UNROLL];
 #pragma unroll
-  for (int k = 0; k < UNROLL; ++k) {
-    const unsigned v = v0 + k * THREADS;
-    if (v < n) {
-      at[k] = row_index(v, per_row, p.magic);
-      ld[k] = __ldcs(reinterpret_cast<const uint4 *>(
-          p.C + ((b * p.src_len_max + p.src_row0 + at[k].t) * p.dc + 8 * at[k].c8)));
-    } else {
-      ld[k] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
+  for (int k = 0; k < UNROLL; ++k)
+    ld[k] = t0 + k * step < p.rows ? __ldcs(reinterpret_cast<const uint4 *>(src + (size_t)(k * step) * p.dc))
+                                   : make_uint4(0u, 0u, 0u, 0u);
+  const long long out = b * p.cache_len_max + row0 + t0;
+  uint8_t *codes = p.codes + out * (p.dc / 2) + 4 * c8, *scales = p.scales + out * (p.dc / kFp4Group) + c8 / 2;
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k) {
     uint32_t w[4] = {ld[k].x, ld[k].y, ld[k].z, ld[k].w};
-    __nv_bfloat162 top2 = __floats2bfloat162_rn(0.f, 0.f);
+    auto top_of = [&]() {
+      const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(as_bf162(w[0] & 0x7fff7fffu), as_bf162(w[1] & 0x7fff7fffu)),
+                                           __hmax2_nan(as_bf162(w[2] & 0x7fff7fffu), as_bf162(w[3] & 0x7fff7fffu)));
+      return __hmax_nan(__low2bfloat16(m), __high2bfloat16(m));
+    };
+    float top = __bfloat162float(top_of());
+    if (top != top) {  // a NaN is held as 0
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162 *>(&w[i]);
-      w[i] &= __heq2_mask(v, v);  // a NaN is held as 0
-      const uint32_t a = w[i] & 0x7fff7fffu;
-      top2 = __hmax2(top2, *reinterpret_cast<const __nv_bfloat162 *>(&a));
+      for (int i = 0; i < 4; ++i) w[i] &= __heq2_mask(as_bf162(w[i]), as_bf162(w[i]));
+      top = __bfloat162float(top_of());
     }
-    float top = fmaxf(__low2float(top2), __high2float(top2));
     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1)) * p.inv_cache_scale;
     const float want = fmaxf(round16(fminf(top, kFp4Max * kFp4ScaleMax) * (1.f / kFp4Max)), kFp4ScaleMin);
-    const __nv_fp8_storage_t sb = __nv_cvt_float_to_fp8(want, __NV_SATFINITE, __NV_E4M3);
-    const float inv = rcp_approx(__low2float(e4m3x2_to_f16((uint16_t)sb)));
+    const uint32_t sb = f32_to_e4m3(want);
+    const float inv = rcp_approx(__low2float(e4m3x2_to_f16((uint16_t)sb))) * p.inv_cache_scale;
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[2 * i] = round16(__uint_as_float(w[i] << 16) * p.inv_cache_scale * inv);
-      x[2 * i + 1] = round16(__uint_as_float(w[i] & 0xffff0000u) * p.inv_cache_scale * inv);
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      // to a multiple of 2^-12: half-way points are multiples of 1/4, and other quotients are 2^-10 or more from them
+      scale_round2(x[2 * i], x[2 * i + 1], inv, 3072.f);
     }
     uint32_t code = f32x8_to_fp4(x);
     // a magnitude that rounds to zero is held as +0
     const uint32_t mag = code & 0x77777777u;
-    code = mag | (code & (((mag | (mag << 1) | (mag << 2) | (mag << 3))) & 0x88888888u));
-    const unsigned v = v0 + k * THREADS;
-    if (v < n) {
-      const long long row = (p.row_of ? (long long)p.row_of[b] : p.row0) + at[k].t;
-      if (row >= 0 && row < p.cache_len_max) {  // rows outside the cache are dropped
-        const long long out = b * p.cache_len_max + row;
-        *reinterpret_cast<uint32_t *>(p.codes + out * (p.dc / 2) + 4 * at[k].c8) = code;
-        if ((at[k].c8 & 1) == 0) p.scales[out * (p.dc / kFp4Group) + at[k].c8 / 2] = (uint8_t)sb;
-      }
+    code = mag | (code & (((mag << 1) | (mag << 2) | (mag << 3)) & 0x88888888u));
+    const int t = t0 + k * step;
+    if (t >= first && t < last) {
+      *reinterpret_cast<uint32_t *>(codes + (size_t)(k * step) * (p.dc / 2)) = code;
+      if ((c8 & 1) == 0) scales[(size_t)(k * step) * (p.dc / kFp4Group)] = (uint8_t)sb;
     }
   }
 }
 
-__global__ void __launch_bounds__(THREADS) dequantize_kernel(const Fp4LoadArgs p) {
-  const unsigned per_row = p.dc / 8;
-  const unsigned n = (unsigned)p.rows * per_row;
-  const unsigned v0 = blockIdx.x * (THREADS * UNROLL) + threadIdx.x;
-  const long long b = blockIdx.y;
+__global__ void __launch_bounds__(MAX_THREADS) dequantize_kernel(const Fp4LoadArgs p) {
+  const int per_row = p.dc / 8, step = blockDim.x / per_row;
+  const int c8 = threadIdx.x % per_row, t0 = blockIdx.x * (step * UNROLL) + threadIdx.x / per_row;
+  const long long b = blockIdx.y, row = b * p.cache_len_max + p.row0 + t0;
+  const uint8_t *codes = p.codes + row * (p.dc / 2) + 4 * c8, *scales = p.scales + row * (p.dc / kFp4Group) + c8 / 2;
   uint32_t code[UNROLL];
   uint8_t sb[UNROLL];
-  RowIndex at[UNROLL];
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k) {
-    const unsigned v = v0 + k * THREADS;
-    if (v < n) {
-      at[k] = row_index(v, per_row, p.magic);
-      const long long row = b * p.cache_len_max + p.row0 + at[k].t;
-      code[k] = __ldcs(reinterpret_cast<const uint32_t *>(p.codes + row * (p.dc / 2) + 4 * at[k].c8));
-      sb[k] = p.scales[row * (p.dc / kFp4Group) + at[k].c8 / 2];
+    if (t0 + k * step < p.rows) {
+      code[k] = __ldcs(reinterpret_cast<const uint32_t *>(codes + (size_t)(k * step) * (p.dc / 2)));
+      sb[k] = scales[(size_t)(k * step) * (p.dc / kFp4Group)];
     }
   }
+  uint16_t *dst = p.C + ((b * p.dst_len_max + p.dst_row0 + t0) * p.dc + 8 * c8);
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k) {
-    if (v0 + k * THREADS < n) {
+    if (t0 + k * step < p.rows) {
       __half2 e[4];
       fp4x8_to_f16(code[k], e);
       const __half2 s = __low2half2(e4m3x2_to_f16((uint16_t)sb[k]));
@@ -142,30 +135,33 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const Fp4LoadArgs p
         const float2 f = __half22float2(__hmul2(e[i], s));
         w[i] = pack_bf16x2(f.x * p.cache_scale, f.y * p.cache_scale);
       }
-      *reinterpret_cast<uint4 *>(p.C + ((b * p.dst_len_max + p.dst_row0 + at[k].t) * p.dc + 8 * at[k].c8)) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(dst + (size_t)(k * step) * p.dc) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
-// One grid row per sequence; the caller's checks keep a sequence's vectors below 2^31.
-static dim3 grid_of(long long B, long long rows, int dc) {
-  return dim3((unsigned)((rows * (dc / 8) + THREADS * UNROLL - 1) / (THREADS * UNROLL)), (unsigned)B);
+// Whole rows per block (at most MAX_THREADS threads), one grid row per sequence.
+static void shape_of(long long B, long long rows, int dc, dim3 *grid, unsigned *threads) {
+  const int per_row = dc / 8, step = MAX_THREADS / per_row;
+  *threads = (unsigned)(step * per_row);
+  *grid = dim3((unsigned)((rows + step * UNROLL - 1) / (step * UNROLL)), (unsigned)B);
 }
 
 }  // namespace cache_fp4
 
 int launch_fp4_store(const Fp4StoreArgs &a, cudaStream_t stream) {
-  Fp4StoreArgs p = a;
-  p.magic = cache_fp4::row_magic(a.dc);
-  cache_fp4::quantize_kernel<<<cache_fp4::grid_of(a.B, a.rows, a.dc), cache_fp4::THREADS, 0, stream>>>(p);
+  dim3 grid;
+  unsigned threads;
+  cache_fp4::shape_of(a.B, a.rows, a.dc, &grid, &threads);
+  cache_fp4::quantize_kernel<<<grid, threads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 
 int launch_fp4_load(const Fp4LoadArgs &a, cudaStream_t stream) {
-  Fp4LoadArgs p = a;
-  p.magic = cache_fp4::row_magic(a.dc);
-  cache_fp4::dequantize_kernel<<<cache_fp4::grid_of(a.B, a.rows, a.dc), cache_fp4::THREADS, 0, stream>>>(p);
+  dim3 grid;
+  unsigned threads;
+  cache_fp4::shape_of(a.B, a.rows, a.dc, &grid, &threads);
+  cache_fp4::dequantize_kernel<<<grid, threads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
 

@@ -18,7 +18,6 @@ struct Fp4StoreArgs {
   uint8_t *codes, *scales;  // [B, cache_len_max, dc/2], [B, cache_len_max, dc/16]
   long long cache_len_max, row0;
   const int *row_of;  // optional [B]: first destination row of each sequence
-  unsigned magic;     // set by the launch
 };
 int launch_fp4_store(const Fp4StoreArgs &a, cudaStream_t stream);
 
@@ -29,7 +28,6 @@ struct Fp4LoadArgs {
   float cache_scale;
   uint16_t *C;  // [B, dst_len_max, dc]
   long long dst_len_max, dst_row0;
-  unsigned magic;  // set by the launch
 };
 int launch_fp4_load(const Fp4LoadArgs &a, cudaStream_t stream);
 
