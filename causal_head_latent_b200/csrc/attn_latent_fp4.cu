@@ -123,21 +123,6 @@ __device__ __forceinline__ void tmem_ld24(uint32_t taddr, float (&v)[24]) {
   for (int i = 0; i < 24; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// OR of `v` over the `count` threads of named barrier `id` (all of them must call).
-__device__ __forceinline__ bool bar_or(int id, int count, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(r)
-      : "r"((uint32_t)v), "r"(id), "r"(count)
-      : "memory");
-  return r != 0;
-}
-
-__device__ __forceinline__ void bar_sync(int id, int count) {
-  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
 // Whether some head raised its maximum in tile g (after p_full of g).
 __device__ __forceinline__ bool asks_rescale(const volatile int *rescale_s, int nq, int g) {
   bool any = false;

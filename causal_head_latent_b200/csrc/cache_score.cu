@@ -13,7 +13,7 @@
 //                  sum_h 2^(S - lse_h) per row, added to the score.
 // The weights of a row need every head's log-sum-exp, hence all rows: either the rows are
 // read twice (2 * 1024 bytes at d_c = 512) or S goes out and in (1024 + 2 * 384 at 96
-// heads, and no second run of the MMAs).  S passes through at most 256 MB of workspace,
+// heads, and no second run of the MMAs).  S passes through at most 512 MB of workspace,
 // a group of sequences at a time.
 //
 // scores_kernel.  One CTA per SM, an equal share of the group's 128-row tiles each
@@ -192,15 +192,21 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int i = 0, g = 0; ok && walk.next(batch, &pc); ++i) {
       // q~ lo of the piece (the MMAs of the piece before are done: its last d_full was waited for)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.lo + ((size_t)pc.b * p.H + (head_ok ? h : 0)) * p.dc);
-      for (int kc = 0; kc < nchunk; ++kc) {
+      uint4 w[8], nx[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = head_ok ? src[k] : make_uint4(0u, 0u, 0u, 0u);
+      for (int kc = 0; kc < nchunk; ++kc) {  // the next chunk's loads in flight
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          nx[k] = head_ok && kc + 1 < nchunk ? src[(kc + 1) * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
         float v[32];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint4 w = head_ok ? src[kc * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
-          v[4 * k] = __uint_as_float(w.x);
-          v[4 * k + 1] = __uint_as_float(w.y);
-          v[4 * k + 2] = __uint_as_float(w.z);
-          v[4 * k + 3] = __uint_as_float(w.w);
+          v[4 * k] = __uint_as_float(w[k].x);
+          v[4 * k + 1] = __uint_as_float(w[k].y);
+          v[4 * k + 2] = __uint_as_float(w[k].z);
+          v[4 * k + 3] = __uint_as_float(w[k].w);
+          w[k] = nx[k];
         }
         tmem_st32(tmem + lane_off + TM_LO + kc * 32, v);
       }
@@ -269,16 +275,71 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + 8 * (2 * NSLOT + 8) + 16 + 8 + 16; }
 static_assert(smem_bytes() <= 232448, "dynamic shared memory above the 227 KB a CTA may have");
 
-// Log-sum-exp per head from the pieces' states, then sum_h 2^(S - lse_h) per row.  A block
-// takes `per_block` tiles of a sequence (blockIdx.y); a warp takes sixteen rows at a time, in
-// quads, its lanes the heads, so that S is read in whole 512-byte lines, twelve in flight.
+// Each head's log-sum-exp from the states of a sequence's pieces, by `threads` threads of a
+// block, several per head; the records in a fixed order.  lse: shared or global memory.
+struct JoinParams {
+  ShareBatch batch;
+  long long G;
+  int H, Hp;
+  const float *part_m, *part_l;  // [R, H]
+};
 constexpr int ST = 256;
 
+__device__ __forceinline__ void join_pieces(const JoinParams &p, int b, long long before, long long total, float *m_s,
+                                            float *l_s, float *lse) {
+  const long long G = min(p.G, total);
+  const long long s0 = share_of(before, total, G), s1 = share_of(before + p.batch.tiles(b) - 1, total, G);
+  const int per = ST / p.Hp, h = threadIdx.x % p.Hp, part = threadIdx.x / p.Hp;
+  float m = -INFINITY, l = 0.f;
+  if (part < per && h < p.H) {
+    for (long long s = s0 + part; s <= s1; s += 8 * per) {
+      float pm[8], pl[8], mx = m;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const bool in = s + k * per <= s1;
+        pm[k] = in ? p.part_m[(s + k * per + b) * p.H + h] : -INFINITY;
+        pl[k] = in ? p.part_l[(s + k * per + b) * p.H + h] : 0.f;
+        mx = fmaxf(mx, pm[k]);
+      }
+      l *= m == -INFINITY ? 0.f : exp2f(m - mx);
+      m = mx;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (pm[k] != -INFINITY) l += pl[k] * exp2f(pm[k] - m);
+    }
+  }
+  m_s[threadIdx.x] = m;
+  l_s[threadIdx.x] = l;
+  __syncthreads();
+  if (threadIdx.x < p.H) {
+    for (int k = 1; k < per; ++k) m = fmaxf(m, m_s[threadIdx.x + k * p.Hp]);
+    float sum = 0.f;
+    for (int k = 0; k < per; ++k) {
+      const float mk = m_s[threadIdx.x + k * p.Hp];
+      if (mk != -INFINITY) sum += l_s[threadIdx.x + k * p.Hp] * exp2f(mk - m);
+    }
+    lse[threadIdx.x] = m + log2f(sum);
+  }
+}
+
+__global__ void __launch_bounds__(ST) join_kernel(const JoinParams p, float *lse) {
+  __shared__ long long sums[2];
+  __shared__ float m_s[ST], l_s[ST];
+  const int b = blockIdx.x;
+  long long before, total;
+  block_tile_sums(p.batch, b, sums, &before, &total);
+  if (p.batch.tiles(b) > 0) join_pieces(p, b, before, total, m_s, l_s, lse + (size_t)b * p.H);
+}
+
+// sum_h 2^(S - lse_h) per row, added to the score.  A block takes `per_block` tiles of a
+// sequence (blockIdx.y); a warp takes sixteen rows at a time, in quads, its lanes the heads,
+// so that S is read in whole 512-byte lines, twelve in flight.
+
 struct SumParams {
-  ShareBatch batch;
-  long long G, tiles_max;
-  int H, Hp;
-  const float *part_m, *part_l, *S;
+  JoinParams join;
+  const float *lse;  // null: joined here, by every block
+  long long tiles_max;
+  const float *S;
   float decay;
   float *score;
   long long score_ld;
@@ -287,43 +348,26 @@ struct SumParams {
 
 __global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
   __shared__ long long sums[2];
-  __shared__ float m_s[ST], l_s[ST], lse_s[128];
-  const int b = blockIdx.y;
-  long long before, total;
-  block_tile_sums(p.batch, b, sums, &before, &total);
-  const int len = p.batch.len(b), n = p.batch.tiles(b), tile0 = blockIdx.x * p.per_block;
-  if (tile0 >= n) return;
-  {  // several threads per head share the pieces, then one joins them
-    const long long G = min(p.G, total);
-    const long long s0 = share_of(before, total, G), s1 = share_of(before + n - 1, total, G);
-    const int per = ST / p.Hp, h = threadIdx.x % p.Hp, part = threadIdx.x / p.Hp;
-    float m = -INFINITY, l = 0.f;
-    if (part < per && h < p.H) {
-      for (long long s = s0 + part; s <= s1; s += per) m = fmaxf(m, p.part_m[(s + b) * p.H + h]);
-      if (m != -INFINITY)
-        for (long long s = s0 + part; s <= s1; s += per)
-          l += p.part_l[(s + b) * p.H + h] * exp2f(p.part_m[(s + b) * p.H + h] - m);
-    }
-    m_s[threadIdx.x] = m;
-    l_s[threadIdx.x] = l;
+  __shared__ float m_s[ST], l_s[ST], lse_s[HMAX];
+  const ShareBatch batch = p.join.batch;
+  const int H = p.join.H, Hp = p.join.Hp;
+  const int b = blockIdx.y, tile0 = blockIdx.x * p.per_block;
+  const float *lse_b = p.lse + (size_t)b * H;
+  long long before = 0, total = 0;
+  if (!p.lse) block_tile_sums(batch, b, sums, &before, &total);
+  const int len = batch.len(b);
+  if (tile0 >= batch.tiles(b)) return;
+  if (!p.lse) {
+    join_pieces(p.join, b, before, total, m_s, l_s, lse_s);
     __syncthreads();
-    if (threadIdx.x < p.Hp) {
-      for (int k = 1; k < per; ++k) m = fmaxf(m, m_s[threadIdx.x + k * p.Hp]);
-      float sum = 0.f;
-      for (int k = 0; k < per; ++k) {
-        const float mk = m_s[threadIdx.x + k * p.Hp];
-        if (mk != -INFINITY) sum += l_s[threadIdx.x + k * p.Hp] * exp2f(mk - m);
-      }
-      lse_s[threadIdx.x] = m + log2f(sum);
-    }
-    __syncthreads();
+    lse_b = lse_s;
   }
   const int lane = threadIdx.x & 31;
   float lse[3];
 #pragma unroll
-  for (int i = 0; i < 3; ++i) lse[i] = 32 * i + lane < p.H ? lse_s[32 * i + lane] : 0.f;
+  for (int i = 0; i < 3; ++i) lse[i] = 32 * i + lane < H ? lse_b[32 * i + lane] : 0.f;
   const float4 *S = reinterpret_cast<const float4 *>(p.S) +
-                    ((size_t)b * p.tiles_max + tile0) * (kScoreTileKeys / 4) * p.Hp + lane;
+                    ((size_t)b * p.tiles_max + tile0) * (kScoreTileKeys / 4) * Hp + lane;
   float *score = p.score + (size_t)b * p.score_ld;
   const int rows0 = tile0 * kScoreTileKeys, rows = min(p.per_block * kScoreTileKeys, len - rows0);
   constexpr int Q = 4;  // quads per warp and step
@@ -333,14 +377,14 @@ __global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
     for (int k = 0; k < Q; ++k)
 #pragma unroll
       for (int i = 0; i < 3; ++i)
-        if (r0 + 4 * k < rows && 32 * i + lane < p.H) x[k][i] = __ldcs(S + (size_t)(r0 / 4 + k) * p.Hp + 32 * i);
+        if (r0 + 4 * k < rows && 32 * i + lane < H) x[k][i] = __ldcs(S + (size_t)(r0 / 4 + k) * Hp + 32 * i);
 #pragma unroll
     for (int k = 0; k < Q; ++k) {
       const int r = r0 + 4 * k;
       float v[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        if (r < rows && 32 * i + lane < p.H) {
+        if (r < rows && 32 * i + lane < H) {
           v[0] += fast_exp2(x[k][i].x - lse[i]);
           v[1] += fast_exp2(x[k][i].y - lse[i]);
           v[2] += fast_exp2(x[k][i].z - lse[i]);
@@ -398,20 +442,23 @@ int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
     const long long G = share_count(nb, a.L, KT);
     scores_kernel<<<(unsigned)G, NUM_THREADS, smem_bytes(), stream>>>(tq, tc, p);
     SumParams u;
-    u.batch = p.batch;
-    u.G = G;
+    u.join = JoinParams{p.batch, G, p.H, p.Hp, p.part_m, p.part_l};
     u.tiles_max = p.tiles_max;
-    u.H = p.H;
-    u.Hp = p.Hp;
-    u.part_m = p.part_m;
-    u.part_l = p.part_l;
     u.S = p.S;
     u.decay = a.decay;
     u.score = a.score + (size_t)b0 * a.cache_len_max;
     u.score_ld = a.cache_len_max;
-    // one tile per block until there are eight blocks per SM (each repeats the join of the pieces' states)
+    // one tile per block until there are eight blocks per SM
     const long long per = p.tiles_max * nb / (8 * kShares);
     u.per_block = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
+    // A few pieces per sequence are joined by every block that needs them; many cost less in
+    // a launch of their own (148 pieces: 41 us against 12 + 3 for one sequence of 131072 rows)
+    u.lse = nullptr;
+    if (G > 16ll * nb) {
+      float *lse = reinterpret_cast<float *>(ws + lay.lse);
+      join_kernel<<<nb, ST, 0, stream>>>(u.join, lse);
+      u.lse = lse;
+    }
     sum_kernel<<<dim3((unsigned)((p.tiles_max + u.per_block - 1) / u.per_block), nb), ST, 0, stream>>>(u);
     if (cudaGetLastError() != cudaSuccess) return -1;
   }

@@ -65,7 +65,7 @@ inline size_t fp4_decode_layout_bytes(long long B, long long L, long long H, lon
 // Accumulated weights: the scores of a group of sequences pass through the workspace, as
 // [sequence][tile][key / 4][head, rounded up to 32][key % 4] float32, at most
 // kScoreScratchBytes of them (at least one sequence).
-constexpr long long kScoreScratchBytes = 256ll << 20;
+constexpr long long kScoreScratchBytes = 512ll << 20;
 
 inline long long score_heads(long long H) { return (H + 31) / 32 * 32; }
 inline long long score_tiles(long long L) { return (L + kScoreTileKeys - 1) / kScoreTileKeys; }
@@ -77,9 +77,9 @@ inline long long score_group(long long B, long long L, long long H) {
   return n < 1 ? 1 : n > B ? B : n;
 }
 
-// q~ as bfloat16 hi and lo [B,H,dc] | m, l float [R,H] of a group | the group's scores.
+// q~ as bfloat16 hi and lo [B,H,dc] | of a group: m, l float [R,H], log-sum-exp float [n,H], scores.
 struct ScoreLayout {
-  size_t hi, lo, pm, pl, s, end;
+  size_t hi, lo, pm, pl, lse, s, end;
 };
 inline ScoreLayout score_layout(uintptr_t base, long long B, long long L, long long H, long long dc) {
   const long long n = score_group(B, L, H);
@@ -94,6 +94,8 @@ inline ScoreLayout score_layout(uintptr_t base, long long B, long long L, long l
   off += ws_round(4 * R * H);
   o.pl = off;
   off += ws_round(4 * R * H);
+  o.lse = off;
+  off += ws_round(4 * (size_t)n * H);
   o.s = off;
   off += ws_round((size_t)n * score_seq_bytes(L, H));
   o.end = off;

@@ -165,6 +165,21 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsign
 __device__ __forceinline__ bool warp_wait_relaxed(uint64_t *bar, uint32_t parity, unsigned *status) {
   return __all_sync(0xffffffffu, mbar_wait_relaxed(bar, parity, status)) != 0;
 }
+// OR of `v` over the `count` threads of named barrier `id` (all of them must call).
+__device__ __forceinline__ bool bar_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\tbarrier.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(count)
+      : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void bar_sync(int id, int count) {
+  asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
@@ -187,6 +202,11 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
       "l"(map), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+
+// Programmatic dependent launch: let the next launch of the stream begin, and wait until
+// the launch this one may have begun beside has finished and its writes are visible.
+__device__ __forceinline__ void grid_dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Tiled bulk store of a shared-memory box (laid out as the map's swizzle
 // expects) to global memory; completion is tracked by bulk groups.

@@ -515,7 +515,7 @@ GMLA_API size_t gmla_attend_decode_fp4_workspace_size(int64_t B, int64_t L, int6
  *  decay   finite; 1 accumulates, less than 1 forgets
  *  score   float32 [B, cache_len_max], in/out
  *  workspace >= gmla_cache_score_workspace_size(B, L, H, d_c) bytes, 16-byte
- *          aligned: the scores of a group of sequences pass through it (256 MB, or
+ *          aligned: the scores of a group of sequences pass through it (512 MB, or
  *          one sequence's if that is more).  Calls that may overlap on the GPU need one each.
  * Errors as gmla_attend_decode; GMLA_ERR_ARG also when decay is not finite.
  */

@@ -89,7 +89,7 @@ def test_scale_and_decay(g, scale, decay):
 
 
 def test_several_groups_of_sequences(g):
-    """More sequences than pass through the workspace at once (256 MB: 10 of 65536 rows at 96 heads)."""
+    """More sequences than pass through the workspace at once (512 MB: 21 of 65536 rows at 96 heads)."""
     run(g, 23, 65536, 65536, 96, 64, lens=[65536] + [1000 * k + 7 for k in range(21)] + [0])
 
 
