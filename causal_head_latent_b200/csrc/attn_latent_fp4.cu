@@ -40,7 +40,7 @@
 //
 // Work split: the 48-key tiles of all sequences end to end, cut into 148 equal shares
 // (compact_plan.h), one CTA each; a CTA's pieces (one per sequence it touches) each
-// leave a partial state (m, l, acc) that merge_kernel joins by the exact log-sum-exp
+// leave a partial state (m, l, acc) that merge_wv.cu joins by the exact log-sum-exp
 // rule.  Lengths are read on the device.
 //
 //   warp 0        q~ of the piece's sequence, by TMA
@@ -72,6 +72,7 @@ constexpr int HK = KT / 2;                   // keys per softmax thread
 constexpr int GROUP_WARPS = KT / 16;         // warps per expanding group
 constexpr int FIRST_SOFTMAX = 4, FIRST_STATE = 12, FIRST_EXPAND = 16;
 constexpr int NUM_THREADS = 32 * (FIRST_EXPAND + 4 * GROUP_WARPS);
+constexpr int STORE_WARPS = FIRST_EXPAND - FIRST_SOFTMAX;  // softmax and acc^T warps, three per TMEM quarter
 constexpr int NCHUNK = 8;                    // 64-wide d_c chunks (d_c <= 512)
 constexpr int QCHUNK = HMAX * 128;           // one d_c chunk of q~ for 96 heads
 constexpr int Q_BYTES = NCHUNK * QCHUNK;
@@ -130,6 +131,32 @@ __device__ __forceinline__ bool asks_rescale(const volatile int *rescale_s, int 
   return any;
 }
 
+// This warp's third of its quarter's acc^T (lanes: 32 d_c rows, columns: heads) into the record
+// of sequence b.  One warp per quarter took 18000 cycles for the 192 KB, most of a short call.
+__device__ __forceinline__ void store_acc(const Params &p, uint32_t tmem, int b, int warp, int lane) {
+  tc_fence_after();
+  const int quarter = warp & 3, npairs = (p.dc + 127) / 128, nq = (p.H + 31) / 32;
+  const size_t rec = ((size_t)blockIdx.x + b) * p.H;
+#pragma unroll 1
+  for (int i = (warp - FIRST_SOFTMAX) >> 2; i < npairs * nq; i += 3) {
+    const int blk = i / nq, c = 32 * (i % nq), col = blk * 128 + quarter * 32 + lane;  // latent column
+    float a[32];
+    tmem_ld32(tmem + ((uint32_t)(quarter * 32) << 16) + TM_ACC + blk * HMAX + c, a);
+    if (col < p.dc) {
+      float *dst = p.part_acc + (rec + c) * (size_t)p.dc + col;
+      const int n = p.H - c;
+#pragma unroll
+      for (int k = 0; k < 32; ++k) {
+        if (k < n) *dst = a[k];
+        dst += p.dc;
+      }
+    }
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncwarp();
+}
+
 // 32 channels of one cached row: 16 bytes of codes and two scales.
 struct Unit {
   uint4 codes;
@@ -163,6 +190,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   int *rescale_s = start + 2;  // [4]: last tile + 1 at which a head of these 32 raised its maximum
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rescale_s + 4);
 
+  grid_dependents_may_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const ShareBatch batch = p.batch;
   long long unused, total;
@@ -190,7 +218,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(p_full, 2 * nq + 4);
     mbar_init(scaled, 4);
     mbar_init(acc_done, 1);
-    mbar_init(acc_free, 4);
+    mbar_init(acc_free, STORE_WARPS);
     for (int i = 0; i < 4; ++i) rescale_s[i] = 0;
     fence_barrier_init();
   }
@@ -383,10 +411,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
   } else if (warp >= FIRST_STATE) {
     // ------------------------------------------------------------------ acc^T
-    // Rescales acc^T in the rare tile where a head raised its maximum, and stores it at the
-    // end of a piece.  acc^T lanes are d_c rows, columns are heads.
-    const int quarter = warp & 3, row = quarter * 32 + lane;
-    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    // Rescales acc^T in the rare tile where a head raised its maximum; with the softmax
+    // warps, stores it at the end of a piece.  acc^T lanes are d_c rows, columns are heads.
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     if (lane == 0) mbar_arrive(p_full);  // for tile 0: see below
     bool ok = true;
     for (int i = 0, g = 0; ok && walk.next(batch, &pc); ++i) {
@@ -416,25 +443,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
       }
-      if (!ok || !warp_wait(acc_done, i & 1, p.status)) break;
-      tc_fence_after();
-      const size_t rec = ((size_t)blockIdx.x + pc.b) * p.H;
-#pragma unroll 1
-      for (int blk = 0; blk < npairs; ++blk) {
-        const int col = blk * 128 + row;  // latent column
-#pragma unroll 1
-        for (int c = 0; c < p.H; c += 32) {
-          float a[32];
-          tmem_ld32(tmem + lane_off + TM_ACC + blk * HMAX + c, a);
-          if (col < p.dc) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c + k < p.H) p.part_acc[(rec + c + k) * (size_t)p.dc + col] = a[k];
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
+      ok = ok && warp_wait(acc_done, i & 1, p.status);
+      if ((warp & 3) >= nq) ok = !bar_or(5 + (warp & 3), 96, !ok);  // lets two headless softmax warps go on
+      if (!ok) break;
+      store_acc(p, tmem, pc.b, warp, lane);
       if (lane == 0) mbar_arrive(acc_free);
     }
     tc_fence_before();
@@ -528,7 +540,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         p.part_m[rec + h] = m_used;
         p.part_l[rec + h] = l + l_s[h];
       }
+      if (!warp_wait(acc_done, i & 1, p.status)) break;
+      store_acc(p, tmem, pc.b, warp, lane);
+      if (lane == 0) mbar_arrive(acc_free);
     }
+    if (quarter >= nq)  // no head here, but acc^T rows to store; until then a barrier, which does not poll
+      while (walk.next(batch, &pc)) {
+        if (bar_or(5 + quarter, 96, false)) break;
+        store_acc(p, tmem, pc.b, warp, lane);
+        if (lane == 0) mbar_arrive(acc_free);
+      }
+    tc_fence_before();
   }
 
   __syncwarp();
@@ -545,60 +567,6 @@ constexpr size_t smem_bytes() {
 static_assert(smem_bytes() <= 232448, "dynamic shared memory above the 227 KB a CTA may have");
 static_assert((Q_BYTES + P_BYTES) % 1024 == 0, "the ring starts on a 1024-byte boundary");
 
-// Exact log-sum-exp merge of the pieces of each sequence: c^ = sum_i 2^(m_i - M) acc_i /
-// sum_i 2^(m_i - M) l_i, one thread per float4 of [H, d_c], blockIdx.y the sequence.  A
-// sequence without rows gets c^ = 0.  HBM/L2-bound: it reads every partial state once.
-struct MergeParams {
-  ShareBatch batch;
-  long long G;
-  int H, dc;
-  const float *part_m, *part_l, *part_acc;
-  float cache_scale;  // acc is in units of it
-  float *chat;
-};
-constexpr int MT = 256;
-
-__global__ void __launch_bounds__(MT) merge_kernel(const MergeParams p) {
-  __shared__ long long sums[2];
-  const int b = blockIdx.y;
-  long long before, total;
-  block_tile_sums(p.batch, b, sums, &before, &total);
-  const int i4 = blockIdx.x * MT + threadIdx.x, per_row = p.dc / 4;
-  if (i4 >= p.H * per_row) return;
-  const int h = i4 / per_row, n = p.batch.tiles(b);
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-  if (n > 0) {
-    const long long G = min(p.G, total);
-    const long long s0 = share_of(before, total, G), s1 = share_of(before + n - 1, total, G);
-    const float4 *acc = reinterpret_cast<const float4 *>(p.part_acc);
-    float M = -INFINITY;
-    for (long long s = s0; s <= s1; ++s) M = fmaxf(M, p.part_m[(s + b) * p.H + h]);
-    for (long long s = s0; s <= s1; s += 8) {
-      float e[8];
-      float4 v[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const size_t r = (size_t)(min(s + k, s1) + b) * p.H + h;
-        const float m = p.part_m[r];
-        e[k] = (s + k > s1 || m == -INFINITY) ? 0.f : fast_exp2(m - M);
-        v[k] = acc[r * per_row + i4 % per_row];
-        sum += e[k] * p.part_l[r];
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        a.x = fmaf(e[k], v[k].x, a.x);
-        a.y = fmaf(e[k], v[k].y, a.y);
-        a.z = fmaf(e[k], v[k].z, a.z);
-        a.w = fmaf(e[k], v[k].w, a.w);
-      }
-    }
-  }
-  const float inv = n > 0 ? p.cache_scale / sum : 0.f;
-  reinterpret_cast<float4 *>(p.chat)[(size_t)b * p.H * per_row + i4] =
-      make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-}
-
 }  // namespace latent_fp4
 
 int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
@@ -607,7 +575,7 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
   const Fp4DecodeLayout lay = fp4_decode_layout(reinterpret_cast<uintptr_t>(ws), a.B, a.L, a.H, a.dc);
   uint16_t *qt = reinterpret_cast<uint16_t *>(ws + lay.qt);
   float *pm = reinterpret_cast<float *>(ws + lay.pm), *pl = reinterpret_cast<float *>(ws + lay.pl);
-  float *pacc = reinterpret_cast<float *>(ws + lay.pacc), *chat = reinterpret_cast<float *>(ws + lay.chat);
+  float *pacc = reinterpret_cast<float *>(ws + lay.pacc);
   const long long G = share_count(a.B, a.L, KT);
   constexpr float kLog2e = 1.4426950408889634f;
   if (!set_smem_limit_once(reinterpret_cast<const void *>(decode_kernel), (int)smem_bytes(), kSmemLatentFp4)) return -1;
@@ -618,13 +586,13 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
   const long long dq[3] = {a.dc, a.H, a.B}, sq[2] = {a.dc, (long long)a.H * a.dc};
   const unsigned bq[3] = {64, HMAX, 1};
   if (!make_tmap_bf16(&tq, qt, 3, dq, sq, bq)) return -1;  // 2-byte elements, moved as they are
-  const ShareBatch batch{a.lens, a.B, a.L, KT};
-  const Params p{a.codes, a.scales, a.cache_len_max, a.H, a.dc, batch, pm, pl, pacc, a.status};
+  const Params p{a.codes, a.scales, a.cache_len_max, a.H, a.dc, ShareBatch{a.lens, a.B, a.L, KT}, pm, pl, pacc, a.status};
+  // An ordinary launch: begun beside the absorb kernel it gains 1 us at one short sequence
+  // and loses 70 at B=32, L=131072 (measured side by side).
   decode_kernel<<<(unsigned)G, NUM_THREADS, smem_bytes(), stream>>>(tq, p);
-  const MergeParams m{batch, G, a.H, a.dc, pm, pl, pacc, a.cache_scale, chat};
-  merge_kernel<<<dim3((a.H * (a.dc / 4) + MT - 1) / MT, a.B), MT, 0, stream>>>(m);
   if (cudaGetLastError() != cudaSuccess) return -1;
-  return launch_wv_tc(chat, a.Wv, a.G, a.O, a.B, a.H, a.dc, a.status, stream);
+  const MergeWvArgs m{a.lens, a.B, a.L, KT, G, a.H, a.dc, pm, pl, pacc, a.cache_scale, a.Wv, a.G, a.O, a.status};
+  return launch_merge_wv(m, stream);
 }
 
 }  // namespace gmla

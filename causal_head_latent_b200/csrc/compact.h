@@ -9,6 +9,24 @@ namespace gmla {
 // The device status word of the current device (null on a CUDA error).
 unsigned *status_ptr();
 
+// A launch that may begin while the launch before it in the stream still runs, from the moment
+// all of that one's CTAs have called grid_dependents_may_launch(); its kernel calls
+// grid_dependency_wait() before it touches what that one writes.
+template <typename... P, typename... A>
+inline int launch_beside(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A &&...args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -1;
+}
+
 // ---------------------------------------------------------------- 4-bit rows
 struct Fp4StoreArgs {
   const uint16_t *C;  // [B, src_len_max, dc]
@@ -52,6 +70,20 @@ struct Fp4DecodeArgs {
   unsigned *status;
 };
 int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream);
+
+// Its last step: partial states joined, W_v and the gate applied.
+struct MergeWvArgs {
+  const int *lens;
+  int B, L, tile;
+  long long G;  // shares (compact_plan.h)
+  int H, dc;
+  const float *part_m, *part_l, *part_acc;
+  float cache_scale;
+  const uint16_t *Wv, *gate;
+  uint16_t *out;
+  unsigned *status;
+};
+int launch_merge_wv(const MergeWvArgs &a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- accumulated weights
 struct ScoreArgs {

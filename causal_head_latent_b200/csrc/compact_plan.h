@@ -37,9 +37,9 @@ GMLA_PLAN_HD inline long long share_of(long long t, long long tiles, long long G
 // share a record, and G + B - 1 records hold them all.
 inline long long share_records(long long B, long long L, int tile) { return share_count(B, L, tile) + B - 1; }
 
-// 4-bit decode: q~ float16 [B,H,dc] | m, l float [R,H] | acc float [R,H,dc] | c^ float [B,H,dc].
+// 4-bit decode: q~ float16 [B,H,dc] | m, l float [R,H] | acc float [R,H,dc].
 struct Fp4DecodeLayout {
-  size_t qt, pm, pl, pacc, chat, end;
+  size_t qt, pm, pl, pacc, end;
 };
 inline Fp4DecodeLayout fp4_decode_layout(uintptr_t base, long long B, long long L, long long H, long long dc) {
   const size_t R = (size_t)share_records(B, L, kFp4TileKeys);
@@ -53,8 +53,6 @@ inline Fp4DecodeLayout fp4_decode_layout(uintptr_t base, long long B, long long 
   off += ws_round(4 * R * H);
   o.pacc = off;
   off += ws_round(4 * R * H * dc);
-  o.chat = off;
-  off += ws_round(4 * (size_t)B * H * dc);
   o.end = off;
   return o;
 }

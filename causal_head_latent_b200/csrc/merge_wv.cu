@@ -1,0 +1,239 @@
+// End of the 4-bit decode: the pieces' softmax states joined and W_v applied,
+//   c^[b, h] = cache_scale * sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i
+//   o[b, 128h + r] = sigmoid(G[b, 128h + r]) * sum_c W_v[128h + r, c] c^[b, h, c].
+//
+// One CTA per (head, 32 sequences), eight warps.  W_v^(h) (128 KB at d_c = 512) comes into
+// shared memory by TMA before the launch waits for the decode kernel it begins beside
+// (programmatic launch), so its time is hidden.  Then each sequence's pieces are summed in
+// float32, lane l holding the columns 128 * k + 4l .. of every 128: with more than
+// four sequences a warp sums whole sequences, with fewer 2, 4 or 8 warps share the pieces of
+// one and add up through shared memory.  c^ goes into the product as bfloat16 hi + lo (two
+// passes, about 16 bits), D[r, b] on tcgen05 with M = 128, N = 32.
+// Bound by latency at small batches and by reading the partial states at large ones.
+#include "compact.h"
+#include "internal.h"
+#include "ptx.cuh"
+#include "share_walk.cuh"
+
+namespace gmla {
+namespace merge_wv {
+
+constexpr int HD = 128;
+constexpr int NB = 32;                // sequences per CTA (the MMA's N)
+constexpr int WARPS = 8, THREADS = 32 * WARPS;
+constexpr int WCHUNK = 128 * 64 * 2;  // 128 rows x 64 columns of W_v, 128-byte swizzled
+constexpr int MAX_CHUNKS = 8;         // d_c <= 512
+constexpr int BCHUNK = NB * 64 * 2;
+
+struct Smem {
+  uint8_t w[MAX_CHUNKS][WCHUNK];
+  uint8_t hi[MAX_CHUNKS][BCHUNK];  // bf16(c^) of the 32 sequences
+  uint8_t lo[MAX_CHUNKS][BCHUNK];  // bf16(c^ - hi)
+  float part[WARPS][512];          // pieces of one sequence summed by several warps
+  float sum[WARPS], top[WARPS];
+  uint64_t full, done;
+  long long sums[2];
+  uint32_t tmem_base;
+};
+
+struct Params {
+  ShareBatch batch;
+  long long G;
+  int H, dc;
+  const float *part_m, *part_l, *part_acc;  // [R, H], [R, H], [R, H, dc]; record = share + sequence
+  float cache_scale;
+  const uint16_t *gate;
+  uint16_t *out;
+  unsigned *status;
+};
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+__global__ void __launch_bounds__(THREADS, 1) merge_wv_kernel(const __grid_constant__ CUtensorMap tmW, const Params p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int h = blockIdx.x, b0 = blockIdx.y * NB, nb = min(NB, p.batch.B - b0);
+  const int nchunk = p.dc / 64;
+  if (threadIdx.x == 0) {
+    mbar_init(&sm.full, 1);
+    mbar_init(&sm.done, 1);
+    fence_barrier_init();
+    mbar_arrive_expect_tx(&sm.full, (uint32_t)(nchunk * WCHUNK));
+    for (int k = 0; k < nchunk; ++k) tma_load_2d(sm.w[k], &tmW, &sm.full, 64 * k, HD * h);
+  }
+  if (warp == 0) {
+    tmem_alloc(&sm.tmem_base, NB);
+    tmem_relinquish();
+  }
+  // rows of sequences that are not there are zero
+  for (int i = threadIdx.x; i < nchunk * (NB - nb) * 8; i += THREADS) {
+    const int k = i / ((NB - nb) * 8), off = (nb * 8 + i % ((NB - nb) * 8)) * 16;
+    *reinterpret_cast<uint4 *>(sm.hi[k] + off) = make_uint4(0u, 0u, 0u, 0u);
+    *reinterpret_cast<uint4 *>(sm.lo[k] + off) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  long long before, total;
+  block_tile_sums(p.batch, b0, sm.sums, &before, &total);
+  const long long G = min(p.G, total);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  grid_dependency_wait();  // the partial states
+
+  // warps per sequence (a power of two), this warp's first sequence and its place among them
+  const int wps = nb > 4 ? 1 : nb > 2 ? 2 : nb > 1 ? 4 : 8;
+  const int place = warp % wps;
+  const int ncol = p.dc / 128 + (p.dc % 128 ? 1 : 0);  // 128-column blocks
+  int bs = 0;  // sequence up to whose start `before` counts
+  for (int b = 0; b < nb; b += WARPS / wps) {
+    const int mine = b + warp / wps;
+    float m = -INFINITY, l = 0.f;
+    float4 a[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine < nb) {
+      for (; bs < mine; ++bs) before += p.batch.tiles(b0 + bs);
+      const int n = p.batch.tiles(b0 + mine);
+      if (n > 0) {
+        const long long s0 = share_of(before, total, G), s1 = share_of(before + n - 1, total, G);
+        const size_t r0 = (size_t)(b0 + mine) * p.H + h;  // record of share s: s * H + r0
+        for (long long s = s0 + lane; s <= s1; s += 32) m = fmaxf(m, p.part_m[s * p.H + r0]);
+        m = warp_max(m);
+        constexpr int U = 4;
+        for (long long s = s0 + place; s <= s1; s += U * wps) {
+          float e[U];
+          float4 v[U][4];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const long long su = s + u * wps;
+            const size_t r = (size_t)min(su, s1) * p.H + r0;
+            const float mu = p.part_m[r];
+            e[u] = su > s1 || mu == -INFINITY ? 0.f : fast_exp2(mu - m);
+            if (lane == 0) l += e[u] * p.part_l[r];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (128 * k + 4 * lane < p.dc)
+                v[u][k] = __ldcs(reinterpret_cast<const float4 *>(p.part_acc + r * p.dc + 128 * k + 4 * lane));
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (128 * k + 4 * lane < p.dc) {
+                a[k].x = fmaf(e[u], v[u][k].x, a[k].x);
+                a[k].y = fmaf(e[u], v[u][k].y, a[k].y);
+                a[k].z = fmaf(e[u], v[u][k].z, a[k].z);
+                a[k].w = fmaf(e[u], v[u][k].w, a[k].w);
+              }
+        }
+        l = warp_sum(l);
+      }
+    }
+    if (wps > 1) {  // nb <= WARPS / wps: one turn of the loop, every warp in it
+#pragma unroll
+      for (int k = 0; k < 4; ++k) *reinterpret_cast<float4 *>(&sm.part[warp][128 * k + 4 * lane]) = a[k];
+      if (lane == 0) sm.sum[warp] = l;
+      __syncthreads();
+      if (place == 0) {
+        for (int w = 1; w < wps; ++w) {
+          l += sm.sum[warp + w];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 v = *reinterpret_cast<const float4 *>(&sm.part[warp + w][128 * k + 4 * lane]);
+            a[k].x += v.x;
+            a[k].y += v.y;
+            a[k].z += v.z;
+            a[k].w += v.w;
+          }
+        }
+      }
+    }
+    if (mine < nb && place == 0) {
+      // no visible row: l = 0 and c^ = 0
+      const float inv = l != 0.f ? p.cache_scale / l : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (k >= ncol || 128 * k + 4 * lane >= p.dc) continue;
+        const float x[4] = {a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv};
+        uint32_t hw[2], lw[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const __nv_bfloat16 h0 = __float2bfloat16_rn(x[2 * i]), h1 = __float2bfloat16_rn(x[2 * i + 1]);
+          hw[i] = (uint32_t)__bfloat16_as_ushort(h0) | ((uint32_t)__bfloat16_as_ushort(h1) << 16);
+          lw[i] = pack_bf16x2(x[2 * i] - __bfloat162float(h0), x[2 * i + 1] - __bfloat162float(h1));
+        }
+        // column c = 128 k + 4 lane: chunk c / 64, 16-byte slot ((c % 64) / 8) ^ (row % 8), half (c / 4) % 2
+        const int c = 128 * k + 4 * lane;
+        const uint32_t off = mine * 128 + ((((c & 63) >> 3) ^ (mine & 7)) << 4) + ((c >> 2) & 1) * 8;
+        *reinterpret_cast<uint2 *>(sm.hi[c >> 6] + off) = make_uint2(hw[0], hw[1]);
+        *reinterpret_cast<uint2 *>(sm.lo[c >> 6] + off) = make_uint2(lw[0], lw[1]);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    if (mbar_wait(&sm.full, 0, p.status)) {
+      tc_fence_after();
+      constexpr uint32_t idesc = idesc_bf16_f32(128, NB, false, false);
+      for (int part = 0; part < 2; ++part) {
+        uint8_t(*bsrc)[BCHUNK] = part ? sm.lo : sm.hi;
+        for (int kk = 0; kk < p.dc / 16; ++kk)
+          umma_bf16_ss(tmem, sdesc_sw128(smem_u32(sm.w[kk >> 2]) + (kk & 3) * 32, 16, 1024),
+                       sdesc_sw128(smem_u32(bsrc[kk >> 2]) + (kk & 3) * 32, 16, 1024), idesc, (part > 0 || kk > 0) ? 1u : 0u);
+      }
+    }
+    umma_commit(&sm.done);
+  }
+  __syncwarp();
+  if (warp < 4) {
+    const int r = 32 * warp + lane;  // row of W_v^(h): output channel 128h + r
+    float gate[NB];  // the gate logits first, their loads in flight together
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      gate[j] = p.gate && j < nb ? bf16_to_f32(p.gate[((size_t)(b0 + j) * p.H + h) * HD + r]) : 0.f;
+    const bool ok = warp_wait(&sm.done, 0, p.status);
+    tc_fence_after();
+    float v[32];
+    tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), v);
+    if (ok) {
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        if (j < nb)
+          p.out[((size_t)(b0 + j) * p.H + h) * HD + r] =
+              __bfloat16_as_ushort(__float2bfloat16_rn(p.gate ? v[j] * sigmoidf_(gate[j]) : v[j]));
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, NB);
+  }
+}
+
+}  // namespace merge_wv
+
+int launch_merge_wv(const MergeWvArgs &a, cudaStream_t stream) {
+  using namespace merge_wv;
+  if (!set_smem_limit_once(reinterpret_cast<const void *>(merge_wv_kernel), (int)sizeof(Smem), kSmemMergeWv)) return -1;
+  CUtensorMap tw;
+  const long long dw[2] = {a.dc, (long long)a.H * HD}, sw[1] = {a.dc};
+  const unsigned bw[2] = {64, 128};
+  if (!make_tmap_bf16(&tw, a.Wv, 2, dw, sw, bw)) return -1;
+  const Params p{ShareBatch{a.lens, a.B, a.L, a.tile}, a.G, a.H, a.dc, a.part_m, a.part_l, a.part_acc, a.cache_scale,
+                 a.gate, a.out, a.status};
+  return launch_beside(merge_wv_kernel, dim3(a.H, (a.B + NB - 1) / NB), dim3(THREADS), sizeof(Smem), stream, tw, p);
+}
+
+}  // namespace gmla

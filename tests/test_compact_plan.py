@@ -74,9 +74,9 @@ int main() {
     for (int k = 0; k < 16; ++k) {
       const unsigned long long base = 0x7f0000000000ull + 16 * k;
       const Fp4DecodeLayout o = fp4_decode_layout(base, c[0], c[1], c[2], c[3]);
-      std::printf("%s{\"base\":%llu,\"B\":%lld,\"L\":%lld,\"H\":%lld,\"dc\":%lld,\"R\":%lld,\"at\":[%zu,%zu,%zu,%zu,%zu,%zu],"
+      std::printf("%s{\"base\":%llu,\"B\":%lld,\"L\":%lld,\"H\":%lld,\"dc\":%lld,\"R\":%lld,\"at\":[%zu,%zu,%zu,%zu,%zu],"
                   "\"need\":%zu}", first ? "" : ",", base, c[0], c[1], c[2], c[3],
-                  share_records(c[0], c[1], kFp4TileKeys), o.qt, o.pm, o.pl, o.pacc, o.chat, o.end,
+                  share_records(c[0], c[1], kFp4TileKeys), o.qt, o.pm, o.pl, o.pacc, o.end,
                   fp4_decode_layout_bytes(c[0], c[1], c[2], c[3]));
       first = false;
     }
@@ -104,7 +104,7 @@ def test_fp4_decode_workspace(checked):
     import causal_head_latent_b200 as g
     for c in checked:
         B, H, dc, R, at = c["B"], c["H"], c["dc"], c["R"], c["at"]
-        sizes = [2 * B * H * dc, 4 * R * H, 4 * R * H, 4 * R * H * dc, 4 * B * H * dc]
+        sizes = [2 * B * H * dc, 4 * R * H, 4 * R * H, 4 * R * H * dc]
         assert (c["base"] + at[0]) % 256 == 0
         for k, n in enumerate(sizes):
             assert at[k] % 256 == at[0] % 256 and at[k] + n <= at[k + 1]

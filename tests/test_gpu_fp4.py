@@ -163,7 +163,7 @@ def test_decode_one_length(g, B, L, H, d_c):
     check(*decode_case(g, B, L, L + 3, H, d_c))
 
 
-@pytest.mark.parametrize("lens", [[0], [1, 0, 3], [300, 1, 0, 64, 65, 0, 0, 129], [0, 0, 0, 0], [5000, 2, 2, 2],
+@pytest.mark.parametrize("lens", [[0], [1, 0, 3], [300, 1, 0, 64, 65, 0, 0, 129], [0, 0, 0, 0], [5000, 2, 2, 2], [4999, 5000], [900, 1700, 0, 5000, 333],
                                   [-4, 9999999, 128]])
 def test_decode_ragged(g, lens):
     """Lengths of zero and one, lengths outside 0..L clamped, stored rows past a length never read (NaN scales there)."""
