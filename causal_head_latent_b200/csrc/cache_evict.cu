@@ -10,16 +10,18 @@
 // so every row can move at once.
 //
 // Two launches.
-//  select_kernel  one cluster of CTAs per sequence.  Scores become 32-bit keys in the order
-//     of the rule above (kept in shared memory where they fit); four rounds of 8-bit
-//     histograms, summed over the cluster through distributed shared memory, find the
-//     n-th largest key T and how many keys equal to T stay; ordered scans (a warp owns a
-//     contiguous run of rows and counts by ballots) give every tied row, hole and tail
-//     its rank.  No atomics but the histograms': the result does not depend on order.
-//     Reads 8 bytes a row once (4 without positions).  Bound by latency: about ten
-//     passes over 16K keys per CTA.
-//  move_kernel    copies rows, scores and positions, a warp per row; bound by HBM (elsewhere)
-//     or by reading the index (in place).
+//  select_kernel  one cluster of 8 CTAs per sequence (one CTA up to 8192 rows).  Scores become
+//     32-bit keys in the order of the rule above (kept in shared memory where they fit);
+//     rounds of 8-bit histograms, summed over the cluster through distributed shared
+//     memory, find the n-th largest key, stopping as soon as all keys with the digits so
+//     far are kept (usually after two or three); ordered scans (a warp owns a contiguous
+//     run of rows and counts by ballots) give every tied row, hole and tail its rank.  No
+//     atomics but the histograms': the result does not depend on order.  Bound by latency
+//     and by what 8 SMs take in: 12 bytes a row (4 without positions).  8 x 131072 rows:
+//     28 us (16 CTAs per sequence: 27); 32 x 4097: 11.5 us.
+//  move_kernel    gives each hole the row of its rank, then copies rows, scores and positions, a
+//     warp per row; bound by HBM (elsewhere: 65536 rows of 1 KB in 19 us, 7 TB/s) or by
+//     reading the index (in place).
 #include <cooperative_groups.h>
 
 #include "compact.h"
@@ -31,7 +33,9 @@ namespace cache_evict {
 
 namespace cg = cooperative_groups;
 
-constexpr int THREADS = 512, WARPS = THREADS / 32;
+constexpr int THREADS = 1024, WARPS = THREADS / 32;
+constexpr int HISTS = 8;  // copies of a CTA's histogram, four warps each
+constexpr int U = 4;  // loads and ranking steps in flight per thread: the passes are bound by latency
 
 // The order of floats as unsigned numbers (+0 and -0 equal, a NaN below all).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -55,27 +59,30 @@ struct SelectParams {
 template <int CL>
 __device__ __forceinline__ long long cluster_prefix(long long mine, long long *warp_sum, long long *cta_sum, int rank) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  static_assert(WARPS == 32, "one lane per warp");
   if (lane == 0) warp_sum[warp] = mine;
   __syncthreads();
-  long long before = 0;
-  for (int w = 0; w < warp; ++w) before += warp_sum[w];
+  long long before = 0, all = warp_sum[lane];
+  for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  before = lane < warp ? warp_sum[lane] : 0;
   if (CL > 1) {
-    if (threadIdx.x == THREADS - 1) *cta_sum = before + warp_sum[WARPS - 1];
+    if (threadIdx.x == 0) *cta_sum = all;
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
-    for (int r = 0; r < rank; ++r) before += *cl.map_shared_rank(cta_sum, r);
+    if (lane < rank) before += *cl.map_shared_rank(cta_sum, lane);
     cl.sync();
   } else {
     __syncthreads();
   }
+  for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   return before;
 }
 
 template <int CL>
 __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t keys[];  // [key_cap]
-  __shared__ uint32_t hist[WARPS][256];
-  __shared__ uint32_t bins[256];
+  __shared__ uint32_t hist[HISTS][256];
+  __shared__ uint32_t cta_bins[2][256], bins[256];
   __shared__ long long warp_sum[WARPS], cta_sum;
   __shared__ int newest_s, digit_s;
   __shared__ uint32_t above_s;
@@ -106,6 +113,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   long long newest = len - 1;
   if (pos) {
     int m = INT32_MIN;
+#pragma unroll 8
     for (int i = threadIdx.x; i < cnt; i += THREADS) m = max(m, pos[r0 + i]);
     if (threadIdx.x == 0) newest_s = INT32_MIN;
     __syncthreads();
@@ -114,9 +122,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
     if (CL > 1) {
       cg::cluster_group cl = cg::this_cluster();
       cl.sync();
-      m = INT32_MIN;
-      for (int r = 0; r < CL; ++r) m = max(m, *cl.map_shared_rank(&newest_s, r));
-      newest = m;
+      newest = __reduce_max_sync(0xffffffffu, *cl.map_shared_rank(&newest_s, lane % CL));
       cl.sync();
     } else {
       __syncthreads();
@@ -128,96 +134,126 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
     return at < p.sink || at > newest - p.recent ? kProtected : ordered(score[r0 + i]);
   };
   const bool cached = cnt <= p.key_cap;
-  if (cached)
+  if (cached) {
+#pragma unroll 8
     for (int i = threadIdx.x; i < cnt; i += THREADS) keys[i] = make_key(i);
+  }
   __syncthreads();
   auto key_of = [&](int i) -> uint32_t { return cached ? keys[i] : make_key(i); };
 
-  // ---- the n-th largest key
-  uint32_t prefix = 0, want = (uint32_t)n;  // `want` keys with the prefix's digits are still to be kept
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = lane; i < 256; i += 32) hist[warp][i] = 0;
-    __syncwarp();
+  // ---- the n-th largest key, digit by digit: `want` keys with the prefix's digits are still to be kept
+  uint32_t prefix = 0, want = (uint32_t)n;
+  int shift = 32;
+  bool settled = false, all_ties = false;
+  while (!settled) {
+    shift -= 8;
+    for (int i = threadIdx.x; i < HISTS * 256; i += THREADS) (&hist[0][0])[i] = 0;
+    __syncthreads();
+    uint32_t *mine = hist[warp % HISTS];
+#pragma unroll 4
     for (int i = w0 + lane; i < w1; i += 32) {
       const uint32_t k = key_of(i);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&hist[warp][(k >> shift) & 255], 1u);
+      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&mine[(k >> shift) & 255], 1u);
     }
     __syncthreads();
-    uint32_t c = 0;
+    uint32_t c = 0, *own = cta_bins[shift / 8 & 1];  // two in turn: one cluster barrier a digit
     if (threadIdx.x < 256) {
-      for (int w = 0; w < WARPS; ++w) c += hist[w][threadIdx.x];
-      bins[threadIdx.x] = c;
+#pragma unroll
+      for (int w = 0; w < HISTS; ++w) c += hist[w][threadIdx.x];
+      own[threadIdx.x] = c;
     }
     if (CL > 1) {
       cg::cluster_group cl = cg::this_cluster();
       cl.sync();
       if (threadIdx.x < 256) {
         c = 0;
-        for (int r = 0; r < CL; ++r) c += cl.map_shared_rank(bins, r)[threadIdx.x];
+#pragma unroll
+        for (int r = 0; r < CL; ++r) c += cl.map_shared_rank(own, r)[threadIdx.x];
       }
-      cl.sync();
-      if (threadIdx.x < 256) bins[threadIdx.x] = c;
     }
+    if (threadIdx.x < 256) bins[threadIdx.x] = c;
     __syncthreads();
     if (warp == 0) {  // the digit at which the keys counted from above reach `want`: lane i holds eight digits
-      uint32_t s = 0;
-      for (int k = 0; k < 8; ++k) s += bins[255 - 8 * lane - k];
+      uint32_t v[8], s = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k] = bins[255 - 8 * lane - k];
       uint32_t incl = s;
+#pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const uint32_t up = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += up;
       }
       uint32_t a = incl - s;
       if (a < want && incl >= want) {
-        int k = 0;
-        while (a + bins[255 - 8 * lane - k] < want) a += bins[255 - 8 * lane - k++];
-        digit_s = 255 - 8 * lane - k;
+        int d = -1;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (d < 0 && a + v[k] >= want) d = k;
+          if (d < 0) a += v[k];
+        }
+        digit_s = 255 - 8 * lane - d;
         above_s = a;
       }
     }
     __syncthreads();
     prefix |= (uint32_t)digit_s << shift;
     want -= above_s;
+    // done at the last digit, or when every key with these digits is kept
+    all_ties = bins[digit_s] == want;
+    settled = shift == 0 || all_ties;
   }
-  // hist still holds the last digit's counts: rows of each warp whose key is exactly `prefix`
-  const long long eq_before = cluster_prefix<CL>(hist[warp][prefix & 255], warp_sum, &cta_sum, rank);
+  prefix >>= shift;
+  if (CL > 1) cg::this_cluster().sync();  // the last histogram has been read by every CTA
 
   // ---- holes below n and kept rows at or past n, in row order
   const unsigned below = (1u << lane) - 1;
+  // first tied key of each warp, where some are not kept
+  unsigned ties_before = 0;
+  if (!all_ties) {
+    unsigned t = 0;
+    for (int i = w0 + lane; i < w1; i += 32) t += key_of(i) >> shift == prefix;
+    ties_before = (unsigned)cluster_prefix<CL>(__reduce_add_sync(0xffffffffu, t), warp_sum, &cta_sum, rank);
+  }
   auto walk = [&](auto &&visit) {
-    long long eq = eq_before;
-    for (int i = w0; i < w1; i += 32) {
-      const bool in = i + lane < w1;
-      const uint32_t k = in ? key_of(i + lane) : 0u;
-      const bool tie = in && k == prefix;
-      const unsigned ties = __ballot_sync(0xffffffffu, tie);
-      const bool kept = in && (k > prefix || (tie && eq + __popc(ties & below) < want));
-      eq += __popc(ties);
-      const int row = r0 + i + lane;
-      visit(row, in, __ballot_sync(0xffffffffu, in && row < n && !kept), __ballot_sync(0xffffffffu, kept && row >= n));
+    unsigned eq = ties_before;
+    for (int i0 = w0; i0 < w1; i0 += 32 * U) {
+      uint32_t k[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 32 * u + lane;
+        k[u] = i < w1 ? key_of(i) >> shift : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + 32 * u + lane;
+        bool kept = k[u] >= prefix;
+        if (!all_ties) {
+          const unsigned ties = __ballot_sync(0xffffffffu, i < w1 && k[u] == prefix);
+          kept = k[u] > prefix || (k[u] == prefix && eq + __popc(ties & below) < want);
+          eq += __popc(ties);
+        }
+        visit(r0 + i, i < w1, kept);
+      }
     }
   };
-  long long holes = 0, tails = 0;
-  walk([&](int, bool, unsigned h, unsigned t) {
-    holes += __popc(h);
-    tails += __popc(t);
+  unsigned holes = 0, tails = 0;
+  walk([&](int row, bool in, bool kept) {
+    holes += in && row < n && !kept;
+    tails += in && row >= n && kept;
   });
-  const long long first = cluster_prefix<CL>(holes << 32 | tails, warp_sum, &cta_sum, rank);
-  long long hole = first >> 32, tail = first & 0xffffffffll;
+  holes = __reduce_add_sync(0xffffffffu, holes);
+  tails = __reduce_add_sync(0xffffffffu, tails);
+  const long long first = cluster_prefix<CL>((long long)holes << 32 | tails, warp_sum, &cta_sum, rank);
+  unsigned hole = (unsigned)(first >> 32), tail = (unsigned)first;
   int *tail_rows = p.tail + (size_t)b * p.keep;
-  walk([&](int row, bool in, unsigned h, unsigned t) {
-    if (in && row < n) index[row] = h >> lane & 1 ? (int)(-2 - (hole + __popc(h & below))) : row;
+  walk([&](int row, bool in, bool kept) {
+    const unsigned h = __ballot_sync(0xffffffffu, in && row < n && !kept), t = __ballot_sync(0xffffffffu, in && row >= n && kept);
+    // a hole of rank k is -2 - k for now: move_kernel puts tail_rows[k] there
+    if (in && row < n) index[row] = kept ? row : -2 - (int)(hole + __popc(h & below));
     if (t >> lane & 1) tail_rows[tail + __popc(t & below)] = row;
     hole += __popc(h);
     tail += __popc(t);
   });
-  // the tails' rows of the whole sequence are written: each hole takes the one of its rank
-  if (CL > 1) cg::this_cluster().sync();
-  else __syncthreads();
-  for (int i = w0 + lane; i < w1 && r0 + i < n; i += 32) {
-    const int v = index[r0 + i];
-    if (v < 0) index[r0 + i] = tail_rows[-2 - v];
-  }
   if (rank == 0 && threadIdx.x == 0) p.new_lens[b] = n;
 }
 
@@ -227,7 +263,8 @@ struct MoveParams {
   float *dst_score;
   const int *pos;
   int *dst_pos;
-  const int *index;
+  int *index;
+  const int *tail;  // [B, keep]: rows that fill holes, by rank
   long long ld, dst_ld;
   int keep, rows_per_warp;
   bool in_place;
@@ -258,7 +295,12 @@ __device__ __forceinline__ void copy_row(const void *src, void *dst, int words, 
 __global__ void __launch_bounds__(MT) move_kernel(const MoveParams p) {
   const int lane = threadIdx.x & 31, b = blockIdx.y;
   const long long j0 = ((long long)blockIdx.x * (MT / 32) + threadIdx.x / 32) * p.rows_per_warp;
-  const int mine = lane < p.rows_per_warp && j0 + lane < p.keep ? p.index[(size_t)b * p.keep + j0 + lane] : -1;
+  int mine = -1;
+  if (lane < p.rows_per_warp && j0 + lane < p.keep) {
+    int *at = p.index + (size_t)b * p.keep + j0 + lane;
+    mine = *at;
+    if (mine < -1) *at = mine = p.tail[(size_t)b * p.keep + (-2 - mine)];
+  }
   const bool moves = mine >= 0 && !(p.in_place && mine == j0 + lane);
   const size_t from = (size_t)b * p.ld + max(mine, 0), to = (size_t)b * p.dst_ld + j0 + lane;
   if (moves) {
@@ -334,6 +376,7 @@ int launch_cache_evict(const EvictArgs &a, cudaStream_t stream) {
   m.pos = a.pos;
   m.dst_pos = a.dst_pos;
   m.index = a.index;
+  m.tail = s.tail;
   m.ld = a.cache_len_max;
   m.dst_ld = a.dst_len_max;
   m.keep = a.keep;

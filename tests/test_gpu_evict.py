@@ -75,7 +75,7 @@ def check(g, B, L, Lmax, keep, lens=None, sink=0, recent=0, inplace=True, fp4=Fa
 @pytest.mark.parametrize("inplace", [True, False])
 @pytest.mark.parametrize("B,L,keep", [(1, 1, 1), (1, 2, 1), (2, 33, 32), (3, 100, 7), (1, 100, 100), (2, 100, 130),
                                       (2, 4097, 4096), (5, 999, 500), (1, 8193, 100), (2, 20001, 19000),
-                                      (1, 300000, 100000)])
+                                      (1, 300000, 100000), (1, 400000, 1000)])
 def test_uniform(g, B, L, keep, inplace):
     check(g, B, L, L + 3, keep, sink=min(4, keep // 4), recent=min(64, keep // 2), inplace=inplace, fp4=B == 2)
 
