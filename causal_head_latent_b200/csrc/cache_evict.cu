@@ -27,6 +27,7 @@
 #include "compact.h"
 #include "compact_plan.h"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace gmla {
 namespace cache_evict {
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   __shared__ long long warp_sum[WARPS], cta_sum;
   __shared__ int newest_s, digit_s;
   __shared__ uint32_t above_s;
+  grid_dependents_may_launch();
   const int rank = CL > 1 ? (int)cg::this_cluster().block_rank() : 0;
   const int b = blockIdx.x / CL, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int len = p.lens ? min(max(p.lens[b], 0), p.L) : p.L;
@@ -293,6 +295,7 @@ __device__ __forceinline__ void copy_row(const void *src, void *dst, int words, 
 
 // A warp looks at rows_per_warp entries of the index and copies the rows that move.
 __global__ void __launch_bounds__(MT) move_kernel(const MoveParams p) {
+  grid_dependency_wait();
   const int lane = threadIdx.x & 31, b = blockIdx.y;
   const long long j0 = ((long long)blockIdx.x * (MT / 32) + threadIdx.x / 32) * p.rows_per_warp;
   int mine = -1;
@@ -384,8 +387,7 @@ int launch_cache_evict(const EvictArgs &a, cudaStream_t stream) {
   // in place most rows stay and a warp scans 32 entries; elsewhere every row moves
   m.rows_per_warp = a.in_place ? 32 : 8;
   const long long per_block = (long long)m.rows_per_warp * (MT / 32);
-  move_kernel<<<dim3((unsigned)((a.keep + per_block - 1) / per_block), a.B), MT, 0, stream>>>(m);
-  return cudaGetLastError() == cudaSuccess ? 0 : -1;
+  return launch_beside(true, move_kernel, dim3((unsigned)((a.keep + per_block - 1) / per_block), a.B), dim3(MT), 0, stream, m);
 }
 
 }  // namespace gmla

@@ -9,11 +9,11 @@ namespace gmla {
 // The device status word of the current device (null on a CUDA error).
 unsigned *status_ptr();
 
-// A launch that may begin while the launch before it in the stream still runs, from the moment
-// all of that one's CTAs have called grid_dependents_may_launch(); its kernel calls
-// grid_dependency_wait() before it touches what that one writes.
+// A launch that may (with `beside`) begin while the launch before it in the stream still runs,
+// from the moment all of that one's CTAs have called grid_dependents_may_launch(); its kernel
+// calls grid_dependency_wait() before it touches what that one writes.
 template <typename... P, typename... A>
-inline int launch_beside(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A &&...args) {
+inline int launch_beside(bool beside, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A &&...args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
@@ -23,7 +23,7 @@ inline int launch_beside(void (*kernel)(P...), dim3 grid, dim3 block, size_t sme
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = beside ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? 0 : -1;
 }
 

@@ -233,7 +233,7 @@ int launch_merge_wv(const MergeWvArgs &a, cudaStream_t stream) {
   if (!make_tmap_bf16(&tw, a.Wv, 2, dw, sw, bw)) return -1;
   const Params p{ShareBatch{a.lens, a.B, a.L, a.tile}, a.G, a.H, a.dc, a.part_m, a.part_l, a.part_acc, a.cache_scale,
                  a.gate, a.out, a.status};
-  return launch_beside(merge_wv_kernel, dim3(a.H, (a.B + NB - 1) / NB), dim3(THREADS), sizeof(Smem), stream, tw, p);
+  return launch_beside(true, merge_wv_kernel, dim3(a.H, (a.B + NB - 1) / NB), dim3(THREADS), sizeof(Smem), stream, tw, p);
 }
 
 }  // namespace gmla
