@@ -426,11 +426,12 @@ def gmla_cache_quantize_fp4(C, codes, scales, src_row0=0, rows=None, row0=0, row
     dev = torch.cuda.current_device()
     B, n_src, d_c = _shape(C, "C", 3)
     Lmax = _shape(codes, "codes", 3)[1]
-    n = n_src - src_row0 if rows is None else rows
+    src_row0 = int(src_row0)
+    n = n_src - src_row0 if rows is None else int(rows)
     code = lib.gmla_cache_quantize_fp4(
-        _tensor(C, "C", torch.bfloat16, (B, n_src, d_c), dev), B, n_src, src_row0, n, d_c, cache_scale,
+        _tensor(C, "C", torch.bfloat16, (B, n_src, d_c), dev), B, n_src, src_row0, n, d_c, float(cache_scale),
         _tensor(codes, "codes", torch.uint8, (B, Lmax, d_c // 2), dev),
-        _tensor(scales, "scales", torch.uint8, (B, Lmax, d_c // 16), dev), Lmax, row0,
+        _tensor(scales, "scales", torch.uint8, (B, Lmax, d_c // 16), dev), Lmax, int(row0),
         _tensor(row_of, "row_of", torch.int32, (B,), dev), _raw_stream(stream, dev))
     return _check(code, "gmla_cache_quantize_fp4") if check else code
 
@@ -442,11 +443,12 @@ def gmla_cache_dequantize_fp4(codes, scales, C, row0=0, rows=None, dst_row0=0, c
     dev = torch.cuda.current_device()
     B, n_dst, d_c = _shape(C, "C", 3)
     Lmax = _shape(codes, "codes", 3)[1]
-    n = Lmax - row0 if rows is None else rows
+    row0 = int(row0)
+    n = Lmax - row0 if rows is None else int(rows)
     code = lib.gmla_cache_dequantize_fp4(
         _tensor(codes, "codes", torch.uint8, (B, Lmax, d_c // 2), dev),
-        _tensor(scales, "scales", torch.uint8, (B, Lmax, d_c // 16), dev), B, Lmax, row0, n, d_c, cache_scale,
-        _tensor(C, "C", torch.bfloat16, (B, n_dst, d_c), dev), n_dst, dst_row0, _raw_stream(stream, dev))
+        _tensor(scales, "scales", torch.uint8, (B, Lmax, d_c // 16), dev), B, Lmax, row0, n, d_c, float(cache_scale),
+        _tensor(C, "C", torch.bfloat16, (B, n_dst, d_c), dev), n_dst, int(dst_row0), _raw_stream(stream, dev))
     return _check(code, "gmla_cache_dequantize_fp4") if check else code
 
 
@@ -460,13 +462,13 @@ def gmla_attend_decode_fp4(Q, codes, scales, L, W_k, W_v, O, num_heads, cache_sc
     tensor of B lengths on the device (at most L)."""
     dev = torch.cuda.current_device()
     B, Lmax, half = _shape(codes, "codes", 3)
-    d, d_c, bf16 = _shape(Q, "Q", 2)[1], 2 * half, torch.bfloat16
+    d, d_c, bf16, H = _shape(Q, "Q", 2)[1], 2 * half, torch.bfloat16, int(num_heads)
     wp, wb = _ws(workspace)
     code = lib.gmla_attend_decode_fp4(
         _tensor(Q, "Q", bf16, (B, d), dev), _tensor(codes, "codes", torch.uint8, (B, Lmax, half), dev),
-        _tensor(scales, "scales", torch.uint8, (B, Lmax, half // 8), dev), cache_scale, B, Lmax, L,
-        _tensor(lens, "lens", torch.int32, (B,), dev), num_heads, _head_width(d, num_heads), d_c,
-        _tensor(W_k, "W_k", bf16, (d, d_c), dev), _tensor(W_v, "W_v", bf16, (d, d_c), dev), scale,
+        _tensor(scales, "scales", torch.uint8, (B, Lmax, half // 8), dev), float(cache_scale), B, Lmax, int(L),
+        _tensor(lens, "lens", torch.int32, (B,), dev), H, _head_width(d, H), d_c,
+        _tensor(W_k, "W_k", bf16, (d, d_c), dev), _tensor(W_v, "W_v", bf16, (d, d_c), dev), float(scale),
         _tensor(G, "G", bf16, (B, d), dev), _tensor(O, "O", bf16, (B, d), dev), wp, wb, _raw_stream(stream, dev))
     return _check(code, "gmla_attend_decode_fp4") if check else code
 
@@ -482,12 +484,12 @@ def gmla_cache_score(Q, C, L, W_k, score, num_heads, lens=None, scale=0.0, decay
     B lengths on the device (at most L)."""
     dev = torch.cuda.current_device()
     B, Lmax, d_c = _shape(C, "C", 3)
-    d, bf16 = _shape(Q, "Q", 2)[1], torch.bfloat16
+    d, bf16, H = _shape(Q, "Q", 2)[1], torch.bfloat16, int(num_heads)
     wp, wb = _ws(workspace)
     code = lib.gmla_cache_score(
-        _tensor(Q, "Q", bf16, (B, d), dev), _tensor(C, "C", bf16, (B, Lmax, d_c), dev), B, Lmax, L,
-        _tensor(lens, "lens", torch.int32, (B,), dev), num_heads, _head_width(d, num_heads), d_c,
-        _tensor(W_k, "W_k", bf16, (d, d_c), dev), scale, decay,
+        _tensor(Q, "Q", bf16, (B, d), dev), _tensor(C, "C", bf16, (B, Lmax, d_c), dev), B, Lmax, int(L),
+        _tensor(lens, "lens", torch.int32, (B,), dev), H, _head_width(d, H), d_c,
+        _tensor(W_k, "W_k", bf16, (d, d_c), dev), float(scale), float(decay),
         _tensor(score, "score", torch.float32, (B, Lmax), dev), wp, wb, _raw_stream(stream, dev))
     return _check(code, "gmla_cache_score") if check else code
 
@@ -502,7 +504,7 @@ def gmla_cache_evict(rows, score, L, keep, index, new_lens, pos=None, lens=None,
     (a bfloat16 cache, or codes and scales); score float32 [B, cache_len_max]; pos int32 [B, cache_len_max] or
     None; dst, dst_score, dst_pos: the same kinds of tensors [B, dst_len_max, ...], or all None for in place;
     outputs index int32 [B, keep] and new_lens int32 [B] (may be lens); see include/gmla.h."""
-    dev = torch.cuda.current_device()
+    dev, keep = torch.cuda.current_device(), int(keep)
     B, Lmax = _shape(score, "score", 2)
     if not 1 <= len(rows) <= 2:
         raise ValueError("rows must hold one or two tensors")
@@ -524,8 +526,8 @@ def gmla_cache_evict(rows, score, L, keep, index, new_lens, pos=None, lens=None,
     code = lib.gmla_cache_evict(
         *arrays, _tensor(score, "score", torch.float32, (B, Lmax), dev),
         _tensor(dst_score, "dst_score", torch.float32, (B, Dmax), dev), _tensor(pos, "pos", torch.int32, (B, Lmax), dev),
-        _tensor(dst_pos, "dst_pos", torch.int32, (B, Dmax), dev), B, Lmax, Dmax, L,
-        _tensor(lens, "lens", torch.int32, (B,), dev), keep, sink, recent,
+        _tensor(dst_pos, "dst_pos", torch.int32, (B, Dmax), dev), B, Lmax, Dmax, int(L),
+        _tensor(lens, "lens", torch.int32, (B,), dev), keep, int(sink), int(recent),
         _tensor(new_lens, "new_lens", torch.int32, (B,), dev), _tensor(index, "index", torch.int32, (B, keep), dev),
         wp, wb, _raw_stream(stream, dev))
     return _check(code, "gmla_cache_evict") if check else code

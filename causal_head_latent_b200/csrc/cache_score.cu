@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
       for (int o = 4; o >= 1; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
       if ((lane & 7) == 0 && r + lane / 8 < rows) {
         float *dst = score + rows0 + r + lane / 8;
-        *dst = fmaf(p.decay, *dst, a);
+        *dst = p.decay != 0.f ? fmaf(p.decay, *dst, a) : a;
       }
     }
   }

@@ -122,3 +122,15 @@ def test_accumulates_over_captured_steps(g):
 def test_twice_gives_the_same_bits(g):
     a = run(g, 4, 2500, 2500, 96, 512, lens=[2500, 1, 900, 64])
     assert torch.equal(a, run(g, 4, 2500, 2500, 96, 512, lens=[2500, 1, 900, 64]))
+
+
+def test_no_decay_overwrites_what_nobody_initialised(g):
+    rng = np.random.default_rng(8)
+    C, Q = rand(rng, 2, 200, 128), rand(rng, 2, 512)
+    W_k = rand(rng, 512, 128) * 128 ** -0.5
+    score = torch.full((2, 200), float("nan"), device="cuda")
+    ws = torch.empty(g.gmla_cache_score_workspace_size(2, 150, 4, 128), dtype=torch.uint8, device="cuda")
+    g.gmla_cache_score(Q, C, 150, W_k, score, 4, decay=0.0, workspace=ws)
+    add = plain(f64(Q), f64(C), [150, 150], f64(W_k), 4)
+    assert np.linalg.norm(f64(score)[:, :150] - add[:, :150]) <= REL * np.linalg.norm(add)
+    assert torch.isnan(score[:, 150:]).all()
