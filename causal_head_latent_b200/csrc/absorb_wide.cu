@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(THREADS)
     absorb_wide_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmQ, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  grid_dependents_may_launch();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int h = blockIdx.x, c0 = blockIdx.y * 128, b0 = blockIdx.z * NB;
   const int nchunk = min(2, (p.dc - c0) / 64);

@@ -185,23 +185,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t *acc_done = scaled + 1;    // value MMAs of the piece done
   uint64_t *acc_free = acc_done + 1;  // partial state of the piece stored
   uint64_t *mma_idle = acc_free + 1;  // [2]
-  long long *sums = reinterpret_cast<long long *>(mma_idle + 2);  // [2]
-  int *start = reinterpret_cast<int *>(sums + 2);                 // first sequence and tile of this share
-  int *rescale_s = start + 2;  // [4]: last tile + 1 at which a head of these 32 raised its maximum
+  int *start = reinterpret_cast<int *>(mma_idle + 2);  // [3]: first sequence, tile and number of tiles of this share
+  int *rescale_s = start + 3;  // [4]: last tile + 1 at which a head of these 32 raised its maximum
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rescale_s + 4);
 
   grid_dependents_may_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const ShareBatch batch = p.batch;
-  long long unused, total;
-  block_tile_sums(batch, 0, sums, &unused, &total);
-  const long long G = min((long long)gridDim.x, total);  // short lengths may leave fewer tiles than CTAs
-  if (blockIdx.x >= G) return;  // the whole CTA, before any barrier
-  const long long t0 = share_begin(blockIdx.x, total, G);
-  const int n_all = (int)(share_begin(blockIdx.x + 1, total, G) - t0);
   const int npairs = (p.dc + 127) / 128;
   const int nq = (p.H + 31) / 32;  // quarters of 32 heads (TMEM lanes) in use
-
   if (threadIdx.x == 0) {
     mbar_init(bar_q, 1);
     mbar_init(q_free, 1);
@@ -222,17 +214,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int i = 0; i < 4; ++i) rescale_s[i] = 0;
     fence_barrier_init();
   }
+  if (warp == 3) {
+    const ShareStart st = warp_share_start(batch, blockIdx.x, gridDim.x);
+    if (lane == 0) {
+      start[0] = st.b;
+      start[1] = st.tile0;
+      start[2] = st.n;
+    }
+  }
+  __syncthreads();
+  const int n_all = start[2];
+  if (n_all == 0) {  // the whole CTA; the launch still ends after the one it may have begun beside
+    grid_dependency_wait();
+    return;
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
-  }
-  if (warp == 3) {
-    int fb, ft;
-    warp_find_tile(batch, t0, &fb, &ft);
-    if (lane == 0) {
-      start[0] = fb;
-      start[1] = ft;
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -244,6 +242,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (warp == 0) {
     if (lane == 0) {
       tma_prefetch_desc(&tmQt);
+      grid_dependency_wait();  // q~ (the other warps read only the caller's cache and lengths)
       for (int i = 0; walk.next(batch, &pc); ++i) {
         if (i > 0 && !mbar_wait(q_free, (i - 1) & 1, p.status)) break;
         mbar_arrive_expect_tx(bar_q, 2 * npairs * QCHUNK);
@@ -562,7 +561,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 constexpr size_t smem_bytes() {
-  return Q_BYTES + P_BYTES + NSLOT * CCHUNK + 4 * HMAX * 4 + 8 * (2 + (2 + NPT) * NTB + 10 + 2) + 6 * 4 + 16;
+  return Q_BYTES + P_BYTES + NSLOT * CCHUNK + 4 * HMAX * 4 + 8 * (2 + (2 + NPT) * NTB + 10) + 8 * 4;
 }
 static_assert(smem_bytes() <= 232448, "dynamic shared memory above the 227 KB a CTA may have");
 static_assert((Q_BYTES + P_BYTES) % 1024 == 0, "the ring starts on a 1024-byte boundary");
@@ -587,10 +586,12 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
   const unsigned bq[3] = {64, HMAX, 1};
   if (!make_tmap_bf16(&tq, qt, 3, dq, sq, bq)) return -1;  // 2-byte elements, moved as they are
   const Params p{a.codes, a.scales, a.cache_len_max, a.H, a.dc, ShareBatch{a.lens, a.B, a.L, KT}, pm, pl, pacc, a.status};
-  // An ordinary launch: begun beside the absorb kernel it gains 1 us at one short sequence
-  // and loses 70 at B=32, L=131072 (measured side by side).
-  decode_kernel<<<(unsigned)G, NUM_THREADS, smem_bytes(), stream>>>(tq, p);
-  if (cudaGetLastError() != cudaSuccess) return -1;
+  // Beginning beside the absorb kernel hides the set-up of a short launch (B=8 ragged to 16384:
+  // 72 us against 76), and slows a long one (B=32, L=131072: 0.96 ms against 0.89).
+  const long long tiles = (long long)a.B * ((a.L + KT - 1) / KT);
+  if (launch_beside(tiles <= 32 * kShares, decode_kernel, dim3((unsigned)G), dim3(NUM_THREADS), smem_bytes(), stream, tq,
+                    p) != 0)
+    return -1;
   const MergeWvArgs m{a.lens, a.B, a.L, KT, G, a.H, a.dc, pm, pl, pacc, a.cache_scale, a.Wv, a.G, a.O, a.status};
   return launch_merge_wv(m, stream);
 }

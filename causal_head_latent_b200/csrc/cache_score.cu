@@ -68,21 +68,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t *d_full = empty + NSLOT;                                    // [2]
   uint64_t *d_free = d_full + 2;                                       // [2]
   uint64_t *q_full = d_free + 2, *q_free = q_full + 1, *lo_full = q_full + 2, *idle = q_full + 3;
-  long long *sums = reinterpret_cast<long long *>(idle + 1);  // [2]
-  int *start = reinterpret_cast<int *>(sums + 2);             // [2]
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 2);
+  int *start = reinterpret_cast<int *>(idle + 1);  // [3]: first sequence, tile and number of tiles of this share
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 3);
 
   grid_dependents_may_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const ShareBatch batch = p.batch;
-  long long unused, total;
-  block_tile_sums(batch, 0, sums, &unused, &total);
-  const long long G = min((long long)gridDim.x, total);
-  if (blockIdx.x >= G) return;  // the whole CTA, before any barrier
-  const long long t0 = share_begin(blockIdx.x, total, G);
-  const int n_all = (int)(share_begin(blockIdx.x + 1, total, G) - t0);
   const int nchunk = p.dc / 64;
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < NSLOT; ++i) {
       mbar_init(&full[i], 1);
@@ -98,17 +90,23 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(idle, 1);
     fence_barrier_init();
   }
+  if (warp == 3) {
+    const ShareStart st = warp_share_start(batch, blockIdx.x, gridDim.x);
+    if (lane == 0) {
+      start[0] = st.b;
+      start[1] = st.tile0;
+      start[2] = st.n;
+    }
+  }
+  __syncthreads();
+  const int n_all = start[2];
+  if (n_all == 0) {  // the whole CTA; the launch still ends after the one it may have begun beside
+    grid_dependency_wait();
+    return;
+  }
   if (warp == 1) {
     tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
-  }
-  if (warp == 3) {
-    int fb, ft;
-    warp_find_tile(batch, t0, &fb, &ft);
-    if (lane == 0) {
-      start[0] = fb;
-      start[1] = ft;
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -177,6 +175,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp == 2) {
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
+      grid_dependency_wait();  // q~ hi
       for (int i = 0; walk.next(batch, &pc); ++i) {
         if (i > 0 && !mbar_wait(q_free, (i - 1) & 1, p.status)) break;
         mbar_arrive_expect_tx(q_full, nchunk * QCHUNK);
@@ -191,6 +190,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     bool ok = true;
     for (int i = 0, g = 0; ok && walk.next(batch, &pc); ++i) {
+      if (i == 0) grid_dependency_wait();
       // q~ lo of the piece (the MMAs of the piece before are done: its last d_full was waited for)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.lo + ((size_t)pc.b * p.H + (head_ok ? h : 0)) * p.dc);
       uint4 w[8], nx[8];
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + 8 * (2 * NSLOT + 8) + 16 + 8 + 16; }
+constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + 8 * (2 * NSLOT + 8) + 16; }
 static_assert(smem_bytes() <= 232448, "dynamic shared memory above the 227 KB a CTA may have");
 
 // Each head's log-sum-exp from the states of a sequence's pieces, by `threads` threads of a
@@ -444,11 +444,12 @@ int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
     p.S = reinterpret_cast<float *>(ws + lay.s);
     p.status = a.status;
     const long long G = share_count(nb, a.L, KT);
-    scores_kernel<<<(unsigned)G, NUM_THREADS, smem_bytes(), stream>>>(tq, tc, p);
-    if (cudaGetLastError() != cudaSuccess) return -1;
-    // Beginning beside a short launch hides 2 us (B=1, L=1001: 24.6 against 26.7); beside a long one it
-    // takes from its bandwidth (B=32, L=131072: 1.49 ms against 1.39).
+    // Beginning beside a short launch hides 2 us (the sums at B=1, L=1001: 24.6 against 26.7); beside a
+    // long one it takes from its bandwidth (B=32, L=131072: 1.49 ms against 1.39).
     const bool beside = p.tiles_max * nb <= 8 * kShares;
+    if (launch_beside(beside && b0 == 0, scores_kernel, dim3((unsigned)G), dim3(NUM_THREADS), smem_bytes(), stream, tq, tc,
+                      p) != 0)
+      return -1;
     SumParams u;
     u.join = JoinParams{p.batch, G, p.H, p.Hp, p.part_m, p.part_l};
     u.tiles_max = p.tiles_max;

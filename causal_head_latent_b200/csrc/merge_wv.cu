@@ -2,11 +2,11 @@
 //   c^[b, h] = cache_scale * sum_i 2^(m_i - M) acc_i / sum_i 2^(m_i - M) l_i
 //   o[b, 128h + r] = sigmoid(G[b, 128h + r]) * sum_c W_v[128h + r, c] c^[b, h, c].
 //
-// One CTA per (head, 32 sequences), eight warps.  W_v^(h) (128 KB at d_c = 512) comes into
+// One CTA per (head, 32 sequences), sixteen warps.  W_v^(h) (128 KB at d_c = 512) comes into
 // shared memory by TMA before the launch waits for the decode kernel it begins beside
 // (programmatic launch), so its time is hidden.  Then each sequence's pieces are summed in
 // float32, lane l holding the columns 128 * k + 4l .. of every 128: with more than
-// four sequences a warp sums whole sequences, with fewer 2, 4 or 8 warps share the pieces of
+// eight sequences a warp sums whole sequences, with fewer 2 to 16 warps share the pieces of
 // one and add up through shared memory.  c^ goes into the product as bfloat16 hi + lo (two
 // passes, about 16 bits), D[r, b] on tcgen05 with M = 128, N = 32.
 // Bound by latency at small batches and by reading the partial states at large ones.
@@ -20,7 +20,7 @@ namespace merge_wv {
 
 constexpr int HD = 128;
 constexpr int NB = 32;                // sequences per CTA (the MMA's N)
-constexpr int WARPS = 8, THREADS = 32 * WARPS;
+constexpr int WARPS = 16, THREADS = 32 * WARPS;
 constexpr int WCHUNK = 128 * 64 * 2;  // 128 rows x 64 columns of W_v, 128-byte swizzled
 constexpr int MAX_CHUNKS = 8;         // d_c <= 512
 constexpr int BCHUNK = NB * 64 * 2;
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(THREADS, 1) merge_wv_kernel(const __grid_const
   grid_dependency_wait();  // the partial states
 
   // warps per sequence (a power of two), this warp's first sequence and its place among them
-  const int wps = nb > 4 ? 1 : nb > 2 ? 2 : nb > 1 ? 4 : 8;
+  const int wps = nb > 8 ? 1 : nb > 4 ? 2 : nb > 2 ? 4 : nb > 1 ? 8 : 16;
   const int place = warp % wps;
   const int ncol = p.dc / 128 + (p.dc % 128 ? 1 : 0);  // 128-column blocks
   int bs = 0;  // sequence up to whose start `before` counts

@@ -40,19 +40,42 @@ __device__ __forceinline__ void block_tile_sums(const ShareBatch &s, int b_end, 
   *total = scratch[1];
 }
 
-// The sequence that holds tile t of a batch (t below the total), and t's place in it.
-// One warp; every lane returns the same.
-__device__ __forceinline__ void warp_find_tile(const ShareBatch &s, long long t, int *b_out, int *tile_out) {
-  if (!s.lens) {
-    const int n = s.tiles(0);
-    *b_out = (int)(t / n);
-    *tile_out = (int)(t % n);
-    return;
-  }
+// Where share `i` of at most `max_shares` begins: its sequence, the tile within it, and how
+// many tiles it has (0: short lengths may leave fewer tiles than shares).  One converged warp;
+// every lane returns the same.
+struct ShareStart {
+  int b, tile0, n;
+};
+__device__ __forceinline__ ShareStart warp_share_start(const ShareBatch &s, long long i, long long max_shares) {
   const int lane = threadIdx.x & 31;
+  ShareStart r{0, 0, 0};
+  long long total;
+  int n0 = 0;  // this lane's sequence of the first 32
+  if (!s.lens) {
+    n0 = s.tiles(0);
+    total = (long long)n0 * s.B;
+  } else {
+    total = 0;
+    for (int b = lane; b < s.B; b += 32) {
+      const int n = s.tiles(b);
+      if (b < 32) n0 = n;
+      total += n;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  const long long G = min(max_shares, total);
+  if (i >= G) return r;
+  const long long t = share_begin(i, total, G);
+  r.n = (int)(share_begin(i + 1, total, G) - t);
+  if (!s.lens) {
+    r.b = (int)(t / n0);
+    r.tile0 = (int)(t % n0);
+    return r;
+  }
   long long base = 0;
   for (int b0 = 0; b0 < s.B; b0 += 32) {
-    const int n = b0 + lane < s.B ? s.tiles(b0 + lane) : 0;
+    const int n = b0 == 0 ? n0 : b0 + lane < s.B ? s.tiles(b0 + lane) : 0;
     long long incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -62,14 +85,13 @@ __device__ __forceinline__ void warp_find_tile(const ShareBatch &s, long long t,
     const unsigned hit = __ballot_sync(0xffffffffu, base + incl > t);
     if (hit) {
       const int src = __ffs(hit) - 1;
-      *b_out = b0 + src;
-      *tile_out = (int)(t - base - __shfl_sync(0xffffffffu, incl - n, src));
-      return;
+      r.b = b0 + src;
+      r.tile0 = (int)(t - base - __shfl_sync(0xffffffffu, incl - n, src));
+      return r;
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
   }
-  *b_out = s.B;  // not reached for t below the total
-  *tile_out = 0;
+  return r;  // not reached: t is below the total
 }
 
 // One piece: tiles [tile0, tile0 + n) of sequence b, whose rows end at `len`.
