@@ -145,24 +145,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     int c = 0;
     for (int i = 0, g = 0; ok && walk.next_uniform(batch, &pc); ++i) {
-      ok = warp_wait(q_full, i & 1, p.status) && warp_wait(lo_full, i & 1, p.status);
+      ok = warp_wait(q_full, i & 1, p.status);
       for (int j = 0; ok && j < pc.n; ++j, ++g) {
         if (g >= 2) ok = warp_wait_relaxed(&d_free[g & 1], ((g - 2) >> 1) & 1, p.status);
         const uint32_t d = tmem + TM_D + (g & 1) * 128;
-        for (int kc = 0; ok && kc < nchunk; ++kc, ++c) {
-          const int slot = c % NSLOT;
-          ok = warp_wait_relaxed(&full[slot], (c / NSLOT) & 1, p.status);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t a = aq + kc * QCHUNK, b = ac + slot * CCHUNK, alo = tmem + TM_LO + kc * 32;
+        // A piece's first tile takes its hi products first, while lo is on its way to TMEM (the ring
+        // holds a whole tile); the others take both per chunk.
+        const int rounds = j == 0 ? 2 : 1;
+        for (int r = 0; ok && r < rounds; ++r) {
+          const bool do_hi = r == 0, do_lo = r == rounds - 1;
+          if (j == 0 && do_lo) ok = warp_wait(lo_full, i & 1, p.status);
+          for (int kc = 0; ok && kc < nchunk; ++kc) {
+            const int slot = (c + kc) % NSLOT;
+            if (do_hi) ok = warp_wait_relaxed(&full[slot], ((c + kc) / NSLOT) & 1, p.status);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a = aq + kc * QCHUNK, b = ac + slot * CCHUNK, alo = tmem + TM_LO + kc * 32;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t db = sdesc_sw128(b + kk * 32, 16, 1024);
-            umma_f16_ss_if(issue, d, sdesc_sw128(a + kk * 32, 16, 1024), db, id, (kc | kk) ? 1u : 0u);
-            umma_f16_ts_if(issue, d, alo + kk * 8, db, id, 1u);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t db = sdesc_sw128(b + kk * 32, 16, 1024);
+              if (do_hi) umma_f16_ss_if(issue, d, sdesc_sw128(a + kk * 32, 16, 1024), db, id, (kc | kk) ? 1u : 0u);
+              if (do_lo) umma_f16_ts_if(issue, d, alo + kk * 8, db, id, 1u);
+            }
+            if (do_lo) umma_commit_if(issue, &empty[slot]);
           }
-          umma_commit_if(issue, &empty[slot]);
         }
+        c += nchunk;
         if (!ok) break;
         umma_commit_if(issue, &d_full[g & 1]);
       }
@@ -193,23 +201,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (i == 0) grid_dependency_wait();
       // q~ lo of the piece (the MMAs of the piece before are done: its last d_full was waited for)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.lo + ((size_t)pc.b * p.H + (head_ok ? h : 0)) * p.dc);
-      uint4 w[8], nx[8];
+#pragma unroll 1
+      for (int k0 = 0; k0 < nchunk; k0 += 4) {  // four chunks' loads in flight
+        uint4 w[4][8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = head_ok ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-      for (int kc = 0; kc < nchunk; ++kc) {  // the next chunk's loads in flight
+        for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          nx[k] = head_ok && kc + 1 < nchunk ? src[(kc + 1) * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
-        float v[32];
+          for (int k = 0; k < 8; ++k)
+            w[c][k] = head_ok && k0 + c < nchunk ? src[(k0 + c) * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          v[4 * k] = __uint_as_float(w[k].x);
-          v[4 * k + 1] = __uint_as_float(w[k].y);
-          v[4 * k + 2] = __uint_as_float(w[k].z);
-          v[4 * k + 3] = __uint_as_float(w[k].w);
-          w[k] = nx[k];
+        for (int c = 0; c < 4; ++c) {
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            v[4 * k] = __uint_as_float(w[c][k].x);
+            v[4 * k + 1] = __uint_as_float(w[c][k].y);
+            v[4 * k + 2] = __uint_as_float(w[c][k].z);
+            v[4 * k + 3] = __uint_as_float(w[c][k].w);
+          }
+          if (k0 + c < nchunk) tmem_st32(tmem + lane_off + TM_LO + (k0 + c) * 32, v);
         }
-        tmem_st32(tmem + lane_off + TM_LO + kc * 32, v);
       }
       tc_fence_before();
       __syncwarp();
