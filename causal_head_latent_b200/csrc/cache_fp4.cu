@@ -56,20 +56,23 @@ __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinter
 // A block covers blockDim.x / (dc/8) whole rows at a time, UNROLL times: a thread keeps its
 // channels 8 * c8 .. and steps by that many rows.
 __global__ void __launch_bounds__(MAX_THREADS) quantize_kernel(const Fp4StoreArgs p) {
-  const int per_row = p.dc / 8, step = blockDim.x / per_row;
-  const int c8 = threadIdx.x % per_row, t0 = blockIdx.x * (step * UNROLL) + threadIdx.x / per_row;
+  const unsigned per_row = p.dc / 8, step = blockDim.x / per_row;
+  const unsigned c8 = threadIdx.x % per_row;
+  const int t0 = (int)(blockIdx.x * (step * UNROLL) + threadIdx.x / per_row), rows = (int)p.rows;
   const long long b = blockIdx.y;
   const long long row0 = p.row_of ? (long long)p.row_of[b] : p.row0;
   // rows that would land outside the cache are dropped: t in [first, last)
   const int first = (int)max(0ll, min(-row0, p.rows)), last = (int)max(0ll, min(p.rows, p.cache_len_max - row0));
   const uint16_t *src = p.C + ((b * p.src_len_max + p.src_row0 + t0) * p.dc + 8 * c8);
+  const unsigned src_step = step * p.dc;
   uint4 ld[UNROLL];
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k)
-    ld[k] = t0 + k * step < p.rows ? __ldcs(reinterpret_cast<const uint4 *>(src + (size_t)(k * step) * p.dc))
-                                   : make_uint4(0u, 0u, 0u, 0u);
+    ld[k] = t0 + k * (int)step < rows ? __ldcs(reinterpret_cast<const uint4 *>(src + k * src_step))
+                                      : make_uint4(0u, 0u, 0u, 0u);
   const long long out = b * p.cache_len_max + row0 + t0;
   uint8_t *codes = p.codes + out * (p.dc / 2) + 4 * c8, *scales = p.scales + out * (p.dc / kFp4Group) + c8 / 2;
+  const bool even = (c8 & 1) == 0;
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k) {
     uint32_t w[4] = {ld[k].x, ld[k].y, ld[k].z, ld[k].w};
@@ -100,11 +103,13 @@ __global__ void __launch_bounds__(MAX_THREADS) quantize_kernel(const Fp4StoreArg
     // a magnitude that rounds to zero is held as +0
     const uint32_t mag = code & 0x77777777u;
     code = mag | (code & (((mag << 1) | (mag << 2) | (mag << 3)) & 0x88888888u));
-    const int t = t0 + k * step;
+    const int t = t0 + k * (int)step;
     if (t >= first && t < last) {
-      *reinterpret_cast<uint32_t *>(codes + (size_t)(k * step) * (p.dc / 2)) = code;
-      if ((c8 & 1) == 0) scales[(size_t)(k * step) * (p.dc / kFp4Group)] = (uint8_t)sb;
+      *reinterpret_cast<uint32_t *>(codes) = code;
+      if (even) *scales = (uint8_t)sb;
     }
+    codes += src_step / 2;
+    scales += src_step / kFp4Group;
   }
 }
 

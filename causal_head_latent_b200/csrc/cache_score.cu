@@ -471,10 +471,11 @@ int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
     // one tile per block until there are eight blocks per SM
     const long long per = p.tiles_max * nb / (8 * kShares);
     u.per_block = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
-    // A few pieces per sequence are joined by every block that needs them; many cost less in
-    // a launch of their own (148 pieces: 41 us against 12 + 3 for one sequence of 131072 rows)
+    // A few pieces per sequence are joined by every block that needs them (B=8, 19 pieces each: 51 us
+    // a call against 53); many cost less in a launch of their own (148 pieces: 41 us against 12 + 3 for
+    // one sequence of 131072 rows).
     u.lse = nullptr;
-    if (G > 16ll * nb) {
+    if (G > 32ll * nb) {
       float *lse = reinterpret_cast<float *>(ws + lay.lse);
       if (launch_beside(beside, join_kernel, dim3(nb), dim3(ST), 0, stream, u.join, lse) != 0) return -1;
       u.lse = lse;
