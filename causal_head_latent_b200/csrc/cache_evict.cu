@@ -18,7 +18,7 @@
 //     run of rows and counts by ballots) give every tied row, hole and tail its rank.  No
 //     atomics but the histograms': the result does not depend on order.  Bound by latency
 //     and by what 8 SMs take in: 12 bytes a row (4 without positions).  8 x 131072 rows:
-//     28 us (16 CTAs per sequence: 27); 32 x 4097: 11.5 us.
+//     25 us (16 CTAs per sequence: no faster); 32 x 4097: 11.4 us.
 //  move_kernel    gives each hole the row of its rank, then copies rows, scores and positions, a
 //     warp per row; bound by HBM (elsewhere: 65536 rows of 1 KB in 19 us, 7 TB/s) or by
 //     reading the index (in place).
@@ -112,11 +112,31 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   const int wper = ((cnt + WARPS - 1) / WARPS + 31) / 32 * 32;
   const int w0 = min(cnt, warp * wper), w1 = min(cnt, w0 + wper);
 
+  const bool cached = cnt <= p.key_cap;
+  // Up to R rows per thread are loaded once, positions and scores together; more (or keys that
+  // do not fit in shared memory) in passes of their own.
+  constexpr int R = 16;
+  const bool once = cached && cnt <= R * THREADS;
+  int at[R];
+  float sc[R];
+  if (once) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      const int i = threadIdx.x + k * THREADS;
+      at[k] = i < cnt ? (pos ? pos[r0 + i] : r0 + i) : INT32_MIN;
+      sc[k] = i < cnt ? score[r0 + i] : 0.f;
+    }
+  }
   long long newest = len - 1;
   if (pos) {
     int m = INT32_MIN;
+    if (once) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) m = max(m, at[k]);
+    } else {
 #pragma unroll 8
-    for (int i = threadIdx.x; i < cnt; i += THREADS) m = max(m, pos[r0 + i]);
+      for (int i = threadIdx.x; i < cnt; i += THREADS) m = max(m, pos[r0 + i]);
+    }
     if (threadIdx.x == 0) newest_s = INT32_MIN;
     __syncthreads();
     m = __reduce_max_sync(0xffffffffu, m);
@@ -131,12 +151,15 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
       newest = newest_s;
     }
   }
-  auto make_key = [&](int i) -> uint32_t {
-    const long long at = pos ? pos[r0 + i] : r0 + i;
-    return at < p.sink || at > newest - p.recent ? kProtected : ordered(score[r0 + i]);
+  auto key_from = [&](long long position, float x) -> uint32_t {
+    return position < p.sink || position > newest - p.recent ? kProtected : ordered(x);
   };
-  const bool cached = cnt <= p.key_cap;
-  if (cached) {
+  auto make_key = [&](int i) { return key_from(pos ? pos[r0 + i] : r0 + i, score[r0 + i]); };
+  if (once) {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (threadIdx.x + k * THREADS < cnt) keys[threadIdx.x + k * THREADS] = key_from(at[k], sc[k]);
+  } else if (cached) {
 #pragma unroll 8
     for (int i = threadIdx.x; i < cnt; i += THREADS) keys[i] = make_key(i);
   }

@@ -11,12 +11,14 @@
 // exact quotient.
 //
 // Both directions are bound by HBM: 2 bytes in and 9/16 byte out per value (or the
-// reverse).  One thread holds 8 channels: a warp's loads and stores are then whole
-// 128-byte lines, and a group's maximum is one shuffle between two lanes.  Four vectors per
-// thread in flight, the same channels of rows a block's height apart.  Storing is bound by
-// instructions before memory, so they are counted: maxima (NaN included) on packed
-// bfloat16, approximate reciprocals (the rounding takes their error too), product and
-// rounding as a packed fma and add, no clamps but the conversions' own.
+// reverse).  524288 rows of 512 channels, 0.69 GB each way: stored in 104 us, read back in
+// 104 us, 6.6 TB/s.  Reading back, a thread holds 8 channels, so that a warp's loads and
+// stores are whole 128-byte lines.  Storing was bound by instructions first (8 channels per
+// thread: 156 a vector of 8 and 175 us; 104 and 127 us once they were counted), so a thread
+// holds a whole group: its maximum (NaN included, on packed bfloat16), scale and reciprocal
+// are found once, product and rounding are a packed fma and add, the conversions do the
+// clamping.  Both keep four vectors in flight, the same channels of rows a block's height
+// apart.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -53,60 +55,66 @@ __device__ __forceinline__ void scale_round2(float &a, float &b, float s, float 
 }
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162 *>(&w); }
 
-// A block covers blockDim.x / (dc/8) whole rows at a time, UNROLL times: a thread keeps its
-// channels 8 * c8 .. and steps by that many rows.
+// A block covers blockDim.x / (dc/16) whole rows at a time, UNROLL times: a thread keeps its
+// group of 16 channels and steps by that many rows.
 __global__ void __launch_bounds__(MAX_THREADS) quantize_kernel(const Fp4StoreArgs p) {
-  const unsigned per_row = p.dc / 8, step = blockDim.x / per_row;
-  const unsigned c8 = threadIdx.x % per_row;
+  const unsigned per_row = p.dc / kFp4Group, step = blockDim.x / per_row;
+  const unsigned grp = threadIdx.x % per_row;
   const int t0 = (int)(blockIdx.x * (step * UNROLL) + threadIdx.x / per_row), rows = (int)p.rows;
   const long long b = blockIdx.y;
   const long long row0 = p.row_of ? (long long)p.row_of[b] : p.row0;
   // rows that would land outside the cache are dropped: t in [first, last)
   const int first = (int)max(0ll, min(-row0, p.rows)), last = (int)max(0ll, min(p.rows, p.cache_len_max - row0));
-  const uint16_t *src = p.C + ((b * p.src_len_max + p.src_row0 + t0) * p.dc + 8 * c8);
+  const uint16_t *src = p.C + ((b * p.src_len_max + p.src_row0 + t0) * p.dc + kFp4Group * grp);
   const unsigned src_step = step * p.dc;
-  uint4 ld[UNROLL];
+  uint4 ld[UNROLL][2];
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k)
-    ld[k] = t0 + k * (int)step < rows ? __ldcs(reinterpret_cast<const uint4 *>(src + k * src_step))
-                                      : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      ld[k][i] = t0 + k * (int)step < rows ? __ldcs(reinterpret_cast<const uint4 *>(src + k * src_step) + i)
+                                           : make_uint4(0u, 0u, 0u, 0u);
   const long long out = b * p.cache_len_max + row0 + t0;
-  uint8_t *codes = p.codes + out * (p.dc / 2) + 4 * c8, *scales = p.scales + out * (p.dc / kFp4Group) + c8 / 2;
-  const bool even = (c8 & 1) == 0;
+  uint8_t *codes = p.codes + out * (p.dc / 2) + 8 * grp, *scales = p.scales + out * (p.dc / kFp4Group) + grp;
 #pragma unroll
   for (int k = 0; k < UNROLL; ++k) {
-    uint32_t w[4] = {ld[k].x, ld[k].y, ld[k].z, ld[k].w};
+    uint32_t w[8] = {ld[k][0].x, ld[k][0].y, ld[k][0].z, ld[k][0].w, ld[k][1].x, ld[k][1].y, ld[k][1].z, ld[k][1].w};
     auto top_of = [&]() {
-      const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(as_bf162(w[0] & 0x7fff7fffu), as_bf162(w[1] & 0x7fff7fffu)),
-                                           __hmax2_nan(as_bf162(w[2] & 0x7fff7fffu), as_bf162(w[3] & 0x7fff7fffu)));
-      return __hmax_nan(__low2bfloat16(m), __high2bfloat16(m));
+      __nv_bfloat162 m = as_bf162(w[0] & 0x7fff7fffu);
+#pragma unroll
+      for (int i = 1; i < 8; ++i) m = __hmax2_nan(m, as_bf162(w[i] & 0x7fff7fffu));
+      return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
     };
-    float top = __bfloat162float(top_of());
+    float top = top_of();
     if (top != top) {  // a NaN is held as 0
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] &= __heq2_mask(as_bf162(w[i]), as_bf162(w[i]));
-      top = __bfloat162float(top_of());
+      for (int i = 0; i < 8; ++i) w[i] &= __heq2_mask(as_bf162(w[i]), as_bf162(w[i]));
+      top = top_of();
     }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1)) * p.inv_cache_scale;
-    const float want = fmaxf(round16(fminf(top, kFp4Max * kFp4ScaleMax) * (1.f / kFp4Max)), kFp4ScaleMin);
+    const float want =
+        fmaxf(round16(fminf(top * p.inv_cache_scale, kFp4Max * kFp4ScaleMax) * (1.f / kFp4Max)), kFp4ScaleMin);
     const uint32_t sb = f32_to_e4m3(want);
     const float inv = rcp_approx(__low2float(e4m3x2_to_f16((uint16_t)sb))) * p.inv_cache_scale;
-    float x[8];
+    uint32_t code[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      // to a multiple of 2^-12: half-way points are multiples of 1/4, and other quotients are 2^-10 or more from them
-      scale_round2(x[2 * i], x[2 * i + 1], inv, 3072.f);
+    for (int j = 0; j < 2; ++j) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[4 * j + i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[4 * j + i] & 0xffff0000u);
+        // to a multiple of 2^-12: half-way points are multiples of 1/4, and other quotients are 2^-10 or more from them
+        scale_round2(x[2 * i], x[2 * i + 1], inv, 3072.f);
+      }
+      code[j] = f32x8_to_fp4(x);
+      // a magnitude that rounds to zero is held as +0
+      const uint32_t mag = code[j] & 0x77777777u;
+      code[j] = mag | (code[j] & (((mag << 1) | (mag << 2) | (mag << 3)) & 0x88888888u));
     }
-    uint32_t code = f32x8_to_fp4(x);
-    // a magnitude that rounds to zero is held as +0
-    const uint32_t mag = code & 0x77777777u;
-    code = mag | (code & (((mag << 1) | (mag << 2) | (mag << 3)) & 0x88888888u));
     const int t = t0 + k * (int)step;
     if (t >= first && t < last) {
-      *reinterpret_cast<uint32_t *>(codes) = code;
-      if (even) *scales = (uint8_t)sb;
+      *reinterpret_cast<uint2 *>(codes) = make_uint2(code[0], code[1]);
+      *scales = (uint8_t)sb;
     }
     codes += src_step / 2;
     scales += src_step / kFp4Group;
@@ -145,9 +153,9 @@ __global__ void __launch_bounds__(MAX_THREADS) dequantize_kernel(const Fp4LoadAr
   }
 }
 
-// Whole rows per block (at most MAX_THREADS threads), one grid row per sequence.
-static void shape_of(long long B, long long rows, int dc, dim3 *grid, unsigned *threads) {
-  const int per_row = dc / 8, step = MAX_THREADS / per_row;
+// Whole rows of `width` channels per thread in a block of at most MAX_THREADS, one grid row per sequence.
+static void shape_of(long long B, long long rows, int dc, int width, dim3 *grid, unsigned *threads) {
+  const int per_row = dc / width, step = MAX_THREADS / per_row;
   *threads = (unsigned)(step * per_row);
   *grid = dim3((unsigned)((rows + step * UNROLL - 1) / (step * UNROLL)), (unsigned)B);
 }
@@ -157,7 +165,7 @@ static void shape_of(long long B, long long rows, int dc, dim3 *grid, unsigned *
 int launch_fp4_store(const Fp4StoreArgs &a, cudaStream_t stream) {
   dim3 grid;
   unsigned threads;
-  cache_fp4::shape_of(a.B, a.rows, a.dc, &grid, &threads);
+  cache_fp4::shape_of(a.B, a.rows, a.dc, kFp4Group, &grid, &threads);
   cache_fp4::quantize_kernel<<<grid, threads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
@@ -165,7 +173,7 @@ int launch_fp4_store(const Fp4StoreArgs &a, cudaStream_t stream) {
 int launch_fp4_load(const Fp4LoadArgs &a, cudaStream_t stream) {
   dim3 grid;
   unsigned threads;
-  cache_fp4::shape_of(a.B, a.rows, a.dc, &grid, &threads);
+  cache_fp4::shape_of(a.B, a.rows, a.dc, 8, &grid, &threads);
   cache_fp4::dequantize_kernel<<<grid, threads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }
