@@ -79,23 +79,29 @@ __global__ void __launch_bounds__(THREADS)
   __syncwarp();
   const bool ok = mbar_wait(&sm.done, 0, p.status);
   tc_fence_after();
-  float v[32];
-  tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), v);
-  const int c = c0 + 32 * warp + lane;
-  if (ok && c < p.dc) {
+  const int c = c0 + 32 * warp + lane, nb = min(NB, p.B - b0);
+  // Eight sequences at a time, in a loop: straight-line code for 32 costs a short call more in
+  // instruction fetches, all of them cold, than it does in work.
+#pragma unroll 1
+  for (int j0 = 0; j0 < nb; j0 += 8) {
+    float v[8];
+    tmem_ld8(tmem + ((uint32_t)(warp * 32) << 16) + j0, v);
+    if (ok && c < p.dc) {
+      size_t i = ((size_t)(b0 + j0) * p.H + h) * p.dc + c;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      if (b0 + j >= p.B) continue;
-      const size_t i = ((size_t)(b0 + j) * p.H + h) * p.dc + c;
-      const float x = v[j] * p.s;
-      if (p.f16) {
-        p.f16[i] = __half_as_ushort(__float2half_rn(x != x ? x : fminf(fmaxf(x, -65504.f), 65504.f)));
-      } else {
-        const __nv_bfloat16 hi = __float2bfloat16_rn(x);
-        p.hi[i] = __bfloat16_as_ushort(hi);
-        p.lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(hi)));
+      for (int j = 0; j < 8; ++j, i += (size_t)p.H * p.dc) {
+        if (j0 + j >= nb) break;
+        const float x = v[j] * p.s;
+        if (p.f16) {
+          p.f16[i] = __half_as_ushort(__float2half_rn(x != x ? x : fminf(fmaxf(x, -65504.f), 65504.f)));
+        } else {
+          const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+          p.hi[i] = __bfloat16_as_ushort(hi);
+          p.lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(hi)));
+        }
       }
     }
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();

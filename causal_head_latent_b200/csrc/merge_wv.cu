@@ -198,20 +198,32 @@ __global__ void __launch_bounds__(THREADS, 1) merge_wv_kernel(const __grid_const
   __syncwarp();
   if (warp < 4) {
     const int r = 32 * warp + lane;  // row of W_v^(h): output channel 128h + r
-    float gate[NB];  // the gate logits first, their loads in flight together
+    const size_t at = ((size_t)b0 * p.H + h) * HD + r, ld = (size_t)p.H * HD;
+    // Eight sequences at a time, the next eight's gate logits in flight; a loop, because
+    // straight-line code for 32 costs a short call more in cold instruction fetches than work.
+    uint16_t gate[8];
+    auto load_gates = [&](int j0) {
 #pragma unroll
-    for (int j = 0; j < NB; ++j)
-      gate[j] = p.gate && j < nb ? bf16_to_f32(p.gate[((size_t)(b0 + j) * p.H + h) * HD + r]) : 0.f;
+      for (int j = 0; j < 8; ++j) gate[j] = p.gate && j0 + j < nb ? p.gate[at + (j0 + j) * ld] : (uint16_t)0;
+    };
+    load_gates(0);
     const bool ok = warp_wait(&sm.done, 0, p.status);
     tc_fence_after();
-    float v[32];
-    tmem_ld32(tmem + ((uint32_t)(warp * 32) << 16), v);
-    if (ok) {
+#pragma unroll 1
+    for (int j0 = 0; j0 < nb; j0 += 8) {
+      float v[8];
+      tmem_ld8(tmem + ((uint32_t)(warp * 32) << 16) + j0, v);
+      if (p.gate) {
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        if (j < nb)
-          p.out[((size_t)(b0 + j) * p.H + h) * HD + r] =
-              __bfloat16_as_ushort(__float2bfloat16_rn(p.gate ? v[j] * sigmoidf_(gate[j]) : v[j]));
+        for (int j = 0; j < 8; ++j) v[j] *= sigmoidf_(bf16_to_f32(gate[j]));
+        load_gates(j0 + 8);
+      }
+      if (ok) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j0 + j < nb) p.out[at + (j0 + j) * ld] = __bfloat16_as_ushort(__float2bfloat16_rn(v[j]));
+      }
+      __syncwarp();
     }
     tc_fence_before();
   }
