@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t *acc_done = scaled + 1;    // value MMAs of the piece done
   uint64_t *acc_free = acc_done + 1;  // partial state of the piece stored
   uint64_t *mma_idle = acc_free + 1;  // [2]
-  int *start = reinterpret_cast<int *>(mma_idle + 2);  // [3]: first sequence, tile and number of tiles of this share
-  int *rescale_s = start + 3;  // [4]: last tile + 1 at which a head of these 32 raised its maximum
+  int *start = reinterpret_cast<int *>(mma_idle + 2);  // [4]: where this share begins (ShareWalk), its tiles
+  int *rescale_s = start + 4;  // [4]: last tile + 1 at which a head of these 32 raised its maximum
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(rescale_s + 4);
 
   grid_dependents_may_launch();
@@ -215,15 +215,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     fence_barrier_init();
   }
   if (warp == 3) {
-    const ShareStart st = warp_share_start(batch, blockIdx.x, gridDim.x);
+    int n;
+    const ShareWalk w = warp_share_start(batch, blockIdx.x, gridDim.x, &n);
     if (lane == 0) {
-      start[0] = st.b;
-      start[1] = st.tile0;
-      start[2] = st.n;
+      start[0] = w.b;
+      start[1] = w.at;
+      start[2] = w.left;
+      start[3] = n;
     }
   }
   __syncthreads();
-  const int n_all = start[2];
+  const int n_all = start[3];
   if (n_all == 0) {  // the whole CTA; the launch still ends after the one it may have begun beside
     grid_dependency_wait();
     return;
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  ShareWalk walk{start[0], start[1], n_all};
+  ShareWalk walk{start[0], start[1], start[2]};
   SharePiece pc{};
 
   if (warp == 0) {
@@ -561,7 +563,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 }
 
 constexpr size_t smem_bytes() {
-  return Q_BYTES + P_BYTES + NSLOT * CCHUNK + 4 * HMAX * 4 + 8 * (2 + (2 + NPT) * NTB + 10) + 8 * 4;
+  return Q_BYTES + P_BYTES + NSLOT * CCHUNK + 4 * HMAX * 4 + 8 * (2 + (2 + NPT) * NTB + 10) + 9 * 4;
 }
 static_assert(smem_bytes() <= 232448, "dynamic shared memory above the 227 KB a CTA may have");
 static_assert((Q_BYTES + P_BYTES) % 1024 == 0, "the ring starts on a 1024-byte boundary");
@@ -575,7 +577,7 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
   uint16_t *qt = reinterpret_cast<uint16_t *>(ws + lay.qt);
   float *pm = reinterpret_cast<float *>(ws + lay.pm), *pl = reinterpret_cast<float *>(ws + lay.pl);
   float *pacc = reinterpret_cast<float *>(ws + lay.pacc);
-  const long long G = share_count(a.B, a.L, KT);
+  const long long G = share_count(a.B, a.L, KT, kFp4PieceTiles);
   constexpr float kLog2e = 1.4426950408889634f;
   if (!set_smem_limit_once(reinterpret_cast<const void *>(decode_kernel), (int)smem_bytes(), kSmemLatentFp4)) return -1;
   if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e * a.cache_scale, qt, nullptr, nullptr, a.status,
@@ -585,14 +587,14 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
   const long long dq[3] = {a.dc, a.H, a.B}, sq[2] = {a.dc, (long long)a.H * a.dc};
   const unsigned bq[3] = {64, HMAX, 1};
   if (!make_tmap_bf16(&tq, qt, 3, dq, sq, bq)) return -1;  // 2-byte elements, moved as they are
-  const Params p{a.codes, a.scales, a.cache_len_max, a.H, a.dc, ShareBatch{a.lens, a.B, a.L, KT}, pm, pl, pacc, a.status};
+  const Params p{a.codes, a.scales, a.cache_len_max, a.H, a.dc, ShareBatch{a.lens, a.B, a.L, KT, kFp4PieceTiles}, pm, pl, pacc, a.status};
   // Beginning beside the absorb kernel hides the set-up of a short launch (B=8 ragged to 16384:
   // 72 us against 76), and slows a long one (B=32, L=131072: 0.96 ms against 0.89).
   const long long tiles = (long long)a.B * ((a.L + KT - 1) / KT);
   if (launch_beside(tiles <= 32 * kShares, decode_kernel, dim3((unsigned)G), dim3(NUM_THREADS), smem_bytes(), stream, tq,
                     p) != 0)
     return -1;
-  const MergeWvArgs m{a.lens, a.B, a.L, KT, G, a.H, a.dc, pm, pl, pacc, a.cache_scale, a.Wv, a.G, a.O, a.status};
+  const MergeWvArgs m{a.lens, a.B, a.L, KT, kFp4PieceTiles, G, a.H, a.dc, pm, pl, pacc, a.cache_scale, a.Wv, a.G, a.O, a.status};
   return launch_merge_wv(m, stream);
 }
 

@@ -68,8 +68,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t *d_full = empty + NSLOT;                                    // [2]
   uint64_t *d_free = d_full + 2;                                       // [2]
   uint64_t *q_full = d_free + 2, *q_free = q_full + 1, *lo_full = q_full + 2, *idle = q_full + 3;
-  int *start = reinterpret_cast<int *>(idle + 1);  // [3]: first sequence, tile and number of tiles of this share
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 3);
+  int *start = reinterpret_cast<int *>(idle + 1);  // [4]: where this share begins (ShareWalk), its tiles
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 4);
 
   grid_dependents_may_launch();
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
@@ -91,15 +91,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     fence_barrier_init();
   }
   if (warp == 3) {
-    const ShareStart st = warp_share_start(batch, blockIdx.x, gridDim.x);
+    int n;
+    const ShareWalk w = warp_share_start(batch, blockIdx.x, gridDim.x, &n);
     if (lane == 0) {
-      start[0] = st.b;
-      start[1] = st.tile0;
-      start[2] = st.n;
+      start[0] = w.b;
+      start[1] = w.at;
+      start[2] = w.left;
+      start[3] = n;
     }
   }
   __syncthreads();
-  const int n_all = start[2];
+  const int n_all = start[3];
   if (n_all == 0) {  // the whole CTA; the launch still ends after the one it may have begun beside
     grid_dependency_wait();
     return;
@@ -112,7 +114,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-  ShareWalk walk{start[0], start[1], n_all};
+  ShareWalk walk{start[0], start[1], start[2]};
   SharePiece pc{};
 
   if (warp == 0) {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + 8 * (2 * NSLOT + 8) + 16; }
+constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + 8 * (2 * NSLOT + 8) + 20; }
 static_assert(smem_bytes() <= 232448, "dynamic shared memory above the 227 KB a CTA may have");
 
 // Each head's log-sum-exp from the states of a sequence's pieces, by `threads` threads of a
@@ -300,7 +302,8 @@ constexpr int ST = 256;
 __device__ __forceinline__ void join_pieces(const JoinParams &p, int b, long long before, long long total, float *m_s,
                                             float *l_s, float *lse) {
   const long long G = min(p.G, total);
-  const long long s0 = share_of(before, total, G), s1 = share_of(before + p.batch.tiles(b) - 1, total, G);
+  long long s0, s1;
+  shares_of(p.batch, before, p.batch.tiles(b), total, G, &s0, &s1);
   const int per = ST / p.Hp, h = threadIdx.x % p.Hp, part = threadIdx.x / p.Hp;
   float m = -INFINITY, l = 0.f;
   if (part < per && h < p.H) {
@@ -339,7 +342,7 @@ __global__ void __launch_bounds__(ST) join_kernel(const JoinParams p, float *lse
   __shared__ float m_s[ST], l_s[ST];
   const int b = blockIdx.x;
   long long before, total;
-  block_tile_sums(p.batch, b, sums, &before, &total);
+  block_place_sums(p.batch, b, sums, &before, &total);
   grid_dependents_may_launch();
   grid_dependency_wait();
   if (p.batch.tiles(b) > 0) join_pieces(p, b, before, total, m_s, l_s, lse + (size_t)b * p.H);
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
   const int b = blockIdx.y, tile0 = blockIdx.x * p.per_block;
   const float *lse_b = p.lse + (size_t)b * H;
   long long before = 0, total = 0;
-  if (!p.lse) block_tile_sums(batch, b, sums, &before, &total);
+  if (!p.lse) block_place_sums(batch, b, sums, &before, &total);
   const int len = batch.len(b);
   grid_dependency_wait();  // before any exit: a launch that may begin beside this one relies on what came before
   if (tile0 >= batch.tiles(b)) return;
@@ -448,13 +451,13 @@ int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
     p.dc = a.dc;
     p.Hp = (int)score_heads(a.H);
     p.tiles_max = score_tiles(a.L);
-    p.batch = ShareBatch{a.lens ? a.lens + b0 : nullptr, nb, a.L, KT};
+    p.batch = ShareBatch{a.lens ? a.lens + b0 : nullptr, nb, a.L, KT, kScorePieceTiles};
     p.lo = lo + (size_t)b0 * a.H * a.dc;
     p.part_m = reinterpret_cast<float *>(ws + lay.pm);
     p.part_l = reinterpret_cast<float *>(ws + lay.pl);
     p.S = reinterpret_cast<float *>(ws + lay.s);
     p.status = a.status;
-    const long long G = share_count(nb, a.L, KT);
+    const long long G = share_count(nb, a.L, KT, kScorePieceTiles);
     // Beginning beside a short launch hides 2 us (the sums at B=1, L=1001: 24.6 against 26.7); beside a
     // long one it takes from its bandwidth (B=32, L=131072: 1.49 ms against 1.39).
     const bool beside = p.tiles_max * nb <= 8 * kShares;

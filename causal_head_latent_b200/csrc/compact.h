@@ -74,7 +74,7 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream);
 // Its last step: partial states joined, W_v and the gate applied.
 struct MergeWvArgs {
   const int *lens;
-  int B, L, tile;
+  int B, L, tile, extra;
   long long G;  // shares (compact_plan.h)
   int H, dc;
   const float *part_m, *part_l, *part_acc;

@@ -18,31 +18,40 @@ namespace gmla {
 constexpr int kFp4TileKeys = 48;     // cached rows per tile of the 4-bit decode
 constexpr int kScoreTileKeys = 128;  // ... and of the accumulated weights
 
-// The tiles of all sequences, laid end to end, are cut into G equal shares, one
-// per CTA, whatever the lengths: CTA i works tiles [share_begin(i), share_begin(i+1)).
-// The lengths live on the device, so G and every buffer depend on sizes alone.
+// The tiles of all sequences, laid end to end, are cut into G equal shares, one per CTA,
+// whatever the lengths: CTA i works the tiles at [share_begin(i), share_begin(i+1)).  The
+// lengths live on the device, so G and every buffer depend on sizes alone.  A CTA that
+// begins another sequence pays for it (its query to load, a state to store), so every
+// sequence that has tiles counts `extra` empty ones before its first: with n tiles it takes
+// n + extra places, and a share may hold fewer tiles than its places, or none.
 constexpr int kShares = 148;  // one CTA per SM of a B200
+constexpr int kFp4PieceTiles = 3, kScorePieceTiles = 2;
 
-inline long long share_count(long long B, long long L, int tile) {
-  const long long tiles = B * ((L + tile - 1) / tile);
-  return tiles < kShares ? (tiles < 1 ? 1 : tiles) : kShares;
+// At most one share per place, so that a short batch still gets a CTA for every tile.
+inline long long share_count(long long B, long long L, int tile, int extra) {
+  const long long places = B * ((L + tile - 1) / tile + extra);
+  return places < kShares ? (places < 1 ? 1 : places) : kShares;
 }
-GMLA_PLAN_HD inline long long share_begin(long long i, long long tiles, long long G) { return i * tiles / G; }
-// The share that holds tile t: the largest i with share_begin(i) <= t.
-GMLA_PLAN_HD inline long long share_of(long long t, long long tiles, long long G) {
-  return ((t + 1) * G - 1) / tiles;
+GMLA_PLAN_HD inline long long share_places(long long tiles, int extra) { return tiles > 0 ? tiles + extra : 0; }
+GMLA_PLAN_HD inline long long share_begin(long long i, long long places, long long G) { return i * places / G; }
+// The share that holds place t: the largest i with share_begin(i) <= t.
+GMLA_PLAN_HD inline long long share_of(long long t, long long places, long long G) {
+  return ((t + 1) * G - 1) / places;
 }
 // Share i's piece of sequence b keeps its partial state in record i + b: along the
-// tiles i and b only grow and every new piece has a larger i or b, so no two pieces
-// share a record, and G + B - 1 records hold them all.
-inline long long share_records(long long B, long long L, int tile) { return share_count(B, L, tile) + B - 1; }
+// places i and b only grow and every new piece has a larger i or b, so no two pieces
+// share a record, and G + B - 1 records hold them all.  Every share between those of a
+// sequence's first and last tile holds a piece of it.
+inline long long share_records(long long B, long long L, int tile, int extra) {
+  return share_count(B, L, tile, extra) + B - 1;
+}
 
 // 4-bit decode: q~ float16 [B,H,dc] | m, l float [R,H] | acc float [R,H,dc].
 struct Fp4DecodeLayout {
   size_t qt, pm, pl, pacc, end;
 };
 inline Fp4DecodeLayout fp4_decode_layout(uintptr_t base, long long B, long long L, long long H, long long dc) {
-  const size_t R = (size_t)share_records(B, L, kFp4TileKeys);
+  const size_t R = (size_t)share_records(B, L, kFp4TileKeys, kFp4PieceTiles);
   Fp4DecodeLayout o;
   size_t off = ws_round(base) - base;
   o.qt = off;
@@ -81,7 +90,7 @@ struct ScoreLayout {
 };
 inline ScoreLayout score_layout(uintptr_t base, long long B, long long L, long long H, long long dc) {
   const long long n = score_group(B, L, H);
-  const size_t R = (size_t)share_records(n, L, kScoreTileKeys);
+  const size_t R = (size_t)share_records(n, L, kScoreTileKeys, kScorePieceTiles);
   ScoreLayout o;
   size_t off = ws_round(base) - base;
   o.hi = off;

@@ -61,7 +61,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 __global__ void __launch_bounds__(THREADS, 1) merge_wv_kernel(const __grid_constant__ CUtensorMap tmW, const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Smem &sm = *reinterpret_cast<Smem *>(smem_raw);
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const int h = blockIdx.x, b0 = blockIdx.y * NB, nb = min(NB, p.batch.B - b0);
   const int nchunk = p.dc / 64;
   if (threadIdx.x == 0) {
@@ -82,18 +82,34 @@ __global__ void __launch_bounds__(THREADS, 1) merge_wv_kernel(const __grid_const
     *reinterpret_cast<uint4 *>(sm.lo[k] + off) = make_uint4(0u, 0u, 0u, 0u);
   }
   long long before, total;
-  block_tile_sums(p.batch, b0, sm.sums, &before, &total);
+  block_place_sums(p.batch, b0, sm.sums, &before, &total);
   const long long G = min(p.G, total);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, sm.tmem_base, 0);
   grid_dependency_wait();  // the partial states
+
+  // c^ of sequence bb, columns c..c+3, from the pieces' sum t and l, as bfloat16 hi and lo: chunk
+  // c / 64, 16-byte slot ((c % 64) / 8) ^ (bb % 8), half (c / 4) % 2.  No visible row: l = 0, c^ = 0.
+  auto put = [&](int bb, int c, float4 t, float l) {
+    const float inv = l != 0.f ? p.cache_scale / l : 0.f;
+    const float x[4] = {t.x * inv, t.y * inv, t.z * inv, t.w * inv};
+    uint32_t hw[2], lw[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __nv_bfloat16 h0 = __float2bfloat16_rn(x[2 * i]), h1 = __float2bfloat16_rn(x[2 * i + 1]);
+      hw[i] = (uint32_t)__bfloat16_as_ushort(h0) | ((uint32_t)__bfloat16_as_ushort(h1) << 16);
+      lw[i] = pack_bf16x2(x[2 * i] - __bfloat162float(h0), x[2 * i + 1] - __bfloat162float(h1));
+    }
+    const uint32_t off = bb * 128 + ((((c & 63) >> 3) ^ (bb & 7)) << 4) + ((c >> 2) & 1) * 8;
+    *reinterpret_cast<uint2 *>(sm.hi[c >> 6] + off) = make_uint2(hw[0], hw[1]);
+    *reinterpret_cast<uint2 *>(sm.lo[c >> 6] + off) = make_uint2(lw[0], lw[1]);
+  };
 
   // warps per sequence (a power of two), this warp's first sequence and its place among them
   const int wps = nb > 8 ? 1 : nb > 4 ? 2 : nb > 2 ? 4 : nb > 1 ? 8 : 16;
   const int place = warp % wps;
-  const int ncol = p.dc / 128 + (p.dc % 128 ? 1 : 0);  // 128-column blocks
   int bs = 0;  // sequence up to whose start `before` counts
   for (int b = 0; b < nb; b += WARPS / wps) {
     const int mine = b + warp / wps;
@@ -102,10 +118,11 @@ __global__ void __launch_bounds__(THREADS, 1) merge_wv_kernel(const __grid_const
 #pragma unroll
     for (int k = 0; k < 4; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     if (mine < nb) {
-      for (; bs < mine; ++bs) before += p.batch.tiles(b0 + bs);
+      for (; bs < mine; ++bs) before += p.batch.places(b0 + bs);
       const int n = p.batch.tiles(b0 + mine);
       if (n > 0) {
-        const long long s0 = share_of(before, total, G), s1 = share_of(before + n - 1, total, G);
+        long long s0, s1;
+        shares_of(p.batch, before, n, total, G, &s0, &s1);
         const size_t r0 = (size_t)(b0 + mine) * p.H + h;  // record of share s: s * H + r0
         for (long long s = s0 + lane; s <= s1; s += 32) m = fmaxf(m, p.part_m[s * p.H + r0]);
         m = warp_max(m);
@@ -144,56 +161,48 @@ __global__ void __launch_bounds__(THREADS, 1) merge_wv_kernel(const __grid_const
       for (int k = 0; k < 4; ++k) *reinterpret_cast<float4 *>(&sm.part[warp][128 * k + 4 * lane]) = a[k];
       if (lane == 0) sm.sum[warp] = l;
       __syncthreads();
-      if (place == 0) {
-        for (int w = 1; w < wps; ++w) {
-          l += sm.sum[warp + w];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float4 v = *reinterpret_cast<const float4 *>(&sm.part[warp + w][128 * k + 4 * lane]);
-            a[k].x += v.x;
-            a[k].y += v.y;
-            a[k].z += v.z;
-            a[k].w += v.w;
-          }
+      // all threads: four columns of a sequence each
+#pragma unroll 1
+      for (int i = threadIdx.x; i < nb * (p.dc / 4); i += THREADS) {
+        const int bb = i / (p.dc / 4), c = 4 * (i % (p.dc / 4));
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+#pragma unroll 4
+        for (int w = bb * wps; w < (bb + 1) * wps; ++w) {
+          const float4 v = *reinterpret_cast<const float4 *>(&sm.part[w][c]);
+          t.x += v.x;
+          t.y += v.y;
+          t.z += v.z;
+          t.w += v.w;
+          sum += sm.sum[w];
         }
+        put(bb, c, t, sum);
       }
-    }
-    if (mine < nb && place == 0) {
-      // no visible row: l = 0 and c^ = 0
-      const float inv = l != 0.f ? p.cache_scale / l : 0.f;
+    } else if (mine < nb) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (k >= ncol || 128 * k + 4 * lane >= p.dc) continue;
-        const float x[4] = {a[k].x * inv, a[k].y * inv, a[k].z * inv, a[k].w * inv};
-        uint32_t hw[2], lw[2];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const __nv_bfloat16 h0 = __float2bfloat16_rn(x[2 * i]), h1 = __float2bfloat16_rn(x[2 * i + 1]);
-          hw[i] = (uint32_t)__bfloat16_as_ushort(h0) | ((uint32_t)__bfloat16_as_ushort(h1) << 16);
-          lw[i] = pack_bf16x2(x[2 * i] - __bfloat162float(h0), x[2 * i + 1] - __bfloat162float(h1));
-        }
-        // column c = 128 k + 4 lane: chunk c / 64, 16-byte slot ((c % 64) / 8) ^ (row % 8), half (c / 4) % 2
-        const int c = 128 * k + 4 * lane;
-        const uint32_t off = mine * 128 + ((((c & 63) >> 3) ^ (mine & 7)) << 4) + ((c >> 2) & 1) * 8;
-        *reinterpret_cast<uint2 *>(sm.hi[c >> 6] + off) = make_uint2(hw[0], hw[1]);
-        *reinterpret_cast<uint2 *>(sm.lo[c >> 6] + off) = make_uint2(lw[0], lw[1]);
-      }
+      for (int k = 0; k < 4; ++k)
+        if (128 * k + 4 * lane < p.dc) put(mine, 128 * k + 4 * lane, a[k], l);
     }
   }
   fence_proxy_async_smem();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    if (mbar_wait(&sm.full, 0, p.status)) {
+  if (warp == 0) {  // converged, one lane predicated: the operands' addresses stay in uniform registers
+    const uint32_t issue = elect_one();
+    if (warp_wait(&sm.full, 0, p.status)) {
       tc_fence_after();
       constexpr uint32_t idesc = idesc_bf16_f32(128, NB, false, false);
-      for (int part = 0; part < 2; ++part) {
-        uint8_t(*bsrc)[BCHUNK] = part ? sm.lo : sm.hi;
-        for (int kk = 0; kk < p.dc / 16; ++kk)
-          umma_bf16_ss(tmem, sdesc_sw128(smem_u32(sm.w[kk >> 2]) + (kk & 3) * 32, 16, 1024),
-                       sdesc_sw128(smem_u32(bsrc[kk >> 2]) + (kk & 3) * 32, 16, 1024), idesc, (part > 0 || kk > 0) ? 1u : 0u);
+      const uint32_t aw = smem_u32(sm.w[0]), ahi = smem_u32(sm.hi[0]), alo = smem_u32(sm.lo[0]);
+#pragma unroll 1
+      for (int k = 0; k < nchunk; ++k) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t a = sdesc_sw128(aw + k * WCHUNK + kk * 32, 16, 1024);
+          umma_f16_ss_if(issue, tmem, a, sdesc_sw128(ahi + k * BCHUNK + kk * 32, 16, 1024), idesc, (k | kk) ? 1u : 0u);
+          umma_f16_ss_if(issue, tmem, a, sdesc_sw128(alo + k * BCHUNK + kk * 32, 16, 1024), idesc, 1u);
+        }
       }
     }
-    umma_commit(&sm.done);
+    umma_commit_if(issue, &sm.done);
   }
   __syncwarp();
   if (warp < 4) {
@@ -243,7 +252,7 @@ int launch_merge_wv(const MergeWvArgs &a, cudaStream_t stream) {
   const long long dw[2] = {a.dc, (long long)a.H * HD}, sw[1] = {a.dc};
   const unsigned bw[2] = {64, 128};
   if (!make_tmap_bf16(&tw, a.Wv, 2, dw, sw, bw)) return -1;
-  const Params p{ShareBatch{a.lens, a.B, a.L, a.tile}, a.G, a.H, a.dc, a.part_m, a.part_l, a.part_acc, a.cache_scale,
+  const Params p{ShareBatch{a.lens, a.B, a.L, a.tile, a.extra}, a.G, a.H, a.dc, a.part_m, a.part_l, a.part_acc, a.cache_scale,
                  a.gate, a.out, a.status};
   return launch_beside(true, merge_wv_kernel, dim3(a.H, (a.B + NB - 1) / NB), dim3(THREADS), sizeof(Smem), stream, tw, p);
 }

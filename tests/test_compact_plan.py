@@ -22,34 +22,42 @@ CHECKER = r"""
 using namespace gmla;
 static int bad(const char *what, long long a, long long b) { std::printf("BAD %s %lld %lld\n", what, a, b); return 1; }
 // Every tile in exactly one piece, records distinct and inside the workspace, share_of() the inverse of
-// share_begin(), as the kernels use them.
-static int shares(const std::vector<long long> &lens, long long L, int tile) {
-  const long long B = (long long)lens.size(), Gmax = share_count(B, L, tile), R = share_records(B, L, tile);
-  std::vector<long long> tiles(B), before(B + 1, 0);
+// share_begin(), every share between a sequence's first and last holding a piece of it, as the kernels use them.
+static int shares(const std::vector<long long> &lens, long long L, int tile, int extra) {
+  const long long B = (long long)lens.size(), Gmax = share_count(B, L, tile, extra), R = share_records(B, L, tile, extra);
+  std::vector<long long> tiles(B), before(B + 1, 0), seen(B, 0);
   for (long long b = 0; b < B; ++b) {
     tiles[b] = (lens[b] + tile - 1) / tile;
-    before[b + 1] = before[b] + tiles[b];
+    before[b + 1] = before[b] + share_places(tiles[b], extra);
   }
   const long long total = before[B], G = Gmax < total ? Gmax : total;
   if (Gmax < 1 || Gmax > kShares) return bad("share count", Gmax, 0);
   std::set<long long> used;
-  long long seen = 0, most = 0, least = 1ll << 60;
+  long long at = 0, most = 0, least = 1ll << 60;
   for (long long i = 0; i < G; ++i) {
     const long long t0 = share_begin(i, total, G), t1 = share_begin(i + 1, total, G);
-    if (t0 != seen || t1 <= t0) return bad("share range", t0, t1);
+    if (t0 != at || t1 <= t0) return bad("share range", t0, t1);
     if (t1 - t0 > most) most = t1 - t0;
     if (t1 - t0 < least) least = t1 - t0;
     for (long long t = t0; t < t1; ++t)
       if (share_of(t, total, G) != i) return bad("share_of", t, i);
     for (long long b = 0; b < B; ++b) {
-      const long long lo = t0 > before[b] ? t0 : before[b], hi = t1 < before[b + 1] ? t1 : before[b + 1];
+      if (tiles[b] == 0) continue;
+      const long long first = before[b] + extra;
+      const long long lo = t0 > first ? t0 : first, hi = t1 < before[b + 1] ? t1 : before[b + 1];
+      const bool inside = i >= share_of(first, total, G) && i <= share_of(first + tiles[b] - 1, total, G);
+      if ((lo < hi) != inside) return bad("share without a piece", i, b);
       if (lo >= hi) continue;
+      if (lo - first != seen[b]) return bad("tiles out of order", lo - first, seen[b]);
+      seen[b] += hi - lo;
       if (!used.insert(i + b).second) return bad("record used twice", i, b);
       if (i + b >= R) return bad("record outside", i + b, R);
     }
-    seen = t1;
+    at = t1;
   }
-  if (seen != total) return bad("tiles left over", seen, total);
+  if (at != total) return bad("places left over", at, total);
+  for (long long b = 0; b < B; ++b)
+    if (seen[b] != tiles[b]) return bad("tiles left over", b, seen[b]);
   if (G > 0 && most - least > 1) return bad("uneven shares", most, least);
   return 0;
 }
@@ -64,7 +72,7 @@ int main() {
             if (kind == 1) x = std::rand() % (L + 1);
             else if (kind == 2) x = std::rand() % 3 ? 0 : 1 + std::rand() % L;
             else if (kind == 3) x = 0;
-          if (shares(lens, L, tile)) return 1;
+          if (shares(lens, L, tile, 0) || shares(lens, L, tile, tile == 48 ? kFp4PieceTiles : kScorePieceTiles)) return 1;
         }
   }
   std::printf("[");
@@ -76,7 +84,7 @@ int main() {
       const Fp4DecodeLayout o = fp4_decode_layout(base, c[0], c[1], c[2], c[3]);
       std::printf("%s{\"base\":%llu,\"B\":%lld,\"L\":%lld,\"H\":%lld,\"dc\":%lld,\"R\":%lld,\"at\":[%zu,%zu,%zu,%zu,%zu],"
                   "\"need\":%zu}", first ? "" : ",", base, c[0], c[1], c[2], c[3],
-                  share_records(c[0], c[1], kFp4TileKeys), o.qt, o.pm, o.pl, o.pacc, o.end,
+                  share_records(c[0], c[1], kFp4TileKeys, kFp4PieceTiles), o.qt, o.pm, o.pl, o.pacc, o.end,
                   fp4_decode_layout_bytes(c[0], c[1], c[2], c[3]));
       first = false;
     }
