@@ -36,7 +36,7 @@ namespace cg = cooperative_groups;
 
 constexpr int THREADS = 1024, WARPS = THREADS / 32;
 constexpr int HISTS = 8;  // copies of a CTA's histogram, four warps each
-constexpr int U = 4;  // loads and ranking steps in flight per thread: the passes are bound by latency
+constexpr int LOADS = 8;  // loads in flight per thread
 
 // The order of floats as unsigned numbers (+0 and -0 equal, a NaN below all).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -56,24 +56,25 @@ struct SelectParams {
 };
 
 // Exclusive ordered sums over the warps of a cluster: `mine` of each warp (of this CTA and
-// those before it).  `warp_sum` and `cta_sum` are shared memory of every CTA.
+// those before it).  `warp_sum` and `cta_sum` are shared memory of every CTA, not written
+// again while another CTA may read them (a slot per call).
 template <int CL>
 __device__ __forceinline__ long long cluster_prefix(long long mine, long long *warp_sum, long long *cta_sum, int rank) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   static_assert(WARPS == 32, "one lane per warp");
   if (lane == 0) warp_sum[warp] = mine;
   __syncthreads();
-  long long before = 0, all = warp_sum[lane];
-  for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  before = lane < warp ? warp_sum[lane] : 0;
+  const long long own = warp_sum[lane];
+  long long before = lane < warp ? own : 0;
   if (CL > 1) {
-    if (threadIdx.x == 0) *cta_sum = all;
     cg::cluster_group cl = cg::this_cluster();
+    if (warp == 0) {
+      long long all = own;
+      for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+      if (lane == 0) *cta_sum = all;
+    }
     cl.sync();
     if (lane < rank) before += *cl.map_shared_rank(cta_sum, lane);
-    cl.sync();
-  } else {
-    __syncthreads();
   }
   for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   return before;
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   extern __shared__ uint32_t keys[];  // [key_cap]
   __shared__ uint32_t hist[HISTS][256];
   __shared__ uint32_t cta_bins[2][256], bins[256];
-  __shared__ long long warp_sum[WARPS], cta_sum;
+  __shared__ long long warp_sum[2][WARPS], cta_sum[2];
   __shared__ int newest_s, digit_s;
   __shared__ uint32_t above_s;
   grid_dependents_may_launch();
@@ -95,9 +96,8 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   int *index = p.index + (size_t)b * p.keep;
   // rows n .. keep of the index, and (nothing to evict) the rows as they are
   const bool all = len <= p.keep;
-  for (long long j = (long long)rank * THREADS + threadIdx.x; j < p.keep; j += CL * THREADS)
-    if (j >= n) index[j] = -1;
-    else if (all) index[j] = (int)j;
+  for (long long j = (all ? 0 : n) + (long long)rank * THREADS + threadIdx.x; j < p.keep; j += CL * THREADS)
+    index[j] = j < n ? (int)j : -1;
   if (all) {
     if (CL > 1) cg::this_cluster().sync();  // every CTA has read lens before new_lens (they may be one array)
     else __syncthreads();
@@ -112,40 +112,34 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   const int wper = ((cnt + WARPS - 1) / WARPS + 31) / 32 * 32;
   const int w0 = min(cnt, warp * wper), w1 = min(cnt, w0 + wper);
 
+  // The newest position, with the scores taken along where they fit.
   const bool cached = cnt <= p.key_cap;
-  // Up to R rows per thread are loaded once, positions and scores together; more (or keys that
-  // do not fit in shared memory) in passes of their own.
-  constexpr int R = 16;
-  const bool once = cached && cnt <= R * THREADS;
-  int at[R];
-  float sc[R];
-  if (once) {
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int i = threadIdx.x + k * THREADS;
-      at[k] = i < cnt ? (pos ? pos[r0 + i] : r0 + i) : INT32_MIN;
-      sc[k] = i < cnt ? score[r0 + i] : 0.f;
-    }
-  }
   long long newest = len - 1;
+  if (threadIdx.x == 0) newest_s = INT32_MIN;
+  for (int i = threadIdx.x; i < HISTS * 256; i += THREADS) (&hist[0][0])[i] = 0;
+  __syncthreads();
   if (pos) {
     int m = INT32_MIN;
-    if (once) {
+    for (int i0 = threadIdx.x; i0 < cnt; i0 += LOADS * THREADS) {
+      float x[LOADS];
 #pragma unroll
-      for (int k = 0; k < R; ++k) m = max(m, at[k]);
-    } else {
-#pragma unroll 8
-      for (int i = threadIdx.x; i < cnt; i += THREADS) m = max(m, pos[r0 + i]);
+      for (int u = 0; u < LOADS; ++u) {
+        const int i = i0 + u * THREADS;
+        if (i < cnt) {
+          m = max(m, pos[r0 + i]);
+          if (cached) x[u] = score[r0 + i];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < LOADS; ++u)
+        if (cached && i0 + u * THREADS < cnt) keys[i0 + u * THREADS] = __float_as_uint(x[u]);
     }
-    if (threadIdx.x == 0) newest_s = INT32_MIN;
-    __syncthreads();
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) atomicMax(&newest_s, m);
     if (CL > 1) {
       cg::cluster_group cl = cg::this_cluster();
       cl.sync();
       newest = __reduce_max_sync(0xffffffffu, *cl.map_shared_rank(&newest_s, lane % CL));
-      cl.sync();
     } else {
       __syncthreads();
       newest = newest_s;
@@ -154,37 +148,46 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   auto key_from = [&](long long position, float x) -> uint32_t {
     return position < p.sink || position > newest - p.recent ? kProtected : ordered(x);
   };
-  auto make_key = [&](int i) { return key_from(pos ? pos[r0 + i] : r0 + i, score[r0 + i]); };
-  if (once) {
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (threadIdx.x + k * THREADS < cnt) keys[threadIdx.x + k * THREADS] = key_from(at[k], sc[k]);
-  } else if (cached) {
-#pragma unroll 8
-    for (int i = threadIdx.x; i < cnt; i += THREADS) keys[i] = make_key(i);
-  }
-  __syncthreads();
-  auto key_of = [&](int i) -> uint32_t { return cached ? keys[i] : make_key(i); };
+  auto key_of = [&](int i) -> uint32_t {
+    return cached ? keys[i] : key_from(pos ? pos[r0 + i] : r0 + i, score[r0 + i]);
+  };
 
   // ---- the n-th largest key, digit by digit: `want` keys with the prefix's digits are still to be kept
   uint32_t prefix = 0, want = (uint32_t)n;
-  int shift = 32;
-  bool settled = false, all_ties = false;
-  while (!settled) {
-    shift -= 8;
-    for (int i = threadIdx.x; i < HISTS * 256; i += THREADS) (&hist[0][0])[i] = 0;
-    __syncthreads();
-    uint32_t *mine = hist[warp % HISTS];
-#pragma unroll 4
-    for (int i = w0 + lane; i < w1; i += 32) {
-      const uint32_t k = key_of(i);
-      if (shift == 24 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&mine[(k >> shift) & 255], 1u);
+  int shift = 24;
+  bool all_ties = false;
+  uint32_t *mine = hist[warp % HISTS];
+  // the first digit, as the keys are made
+  for (int i0 = threadIdx.x; i0 < cnt; i0 += LOADS * THREADS) {
+    int at[LOADS];
+    float x[LOADS];
+#pragma unroll
+    for (int u = 0; u < LOADS; ++u) {
+      const int i = i0 + u * THREADS;
+      if (i < cnt) {
+        at[u] = pos ? pos[r0 + i] : r0 + i;
+        x[u] = cached && pos ? __uint_as_float(keys[i]) : score[r0 + i];
+      }
     }
+#pragma unroll
+    for (int u = 0; u < LOADS; ++u) {
+      const int i = i0 + u * THREADS;
+      if (i < cnt) {
+        const uint32_t k = key_from(at[u], x[u]);
+        if (cached) keys[i] = k;
+        atomicAdd(&mine[k >> 24], 1u);
+      }
+    }
+  }
+  while (true) {
     __syncthreads();
     uint32_t c = 0, *own = cta_bins[shift / 8 & 1];  // two in turn: one cluster barrier a digit
     if (threadIdx.x < 256) {
 #pragma unroll
-      for (int w = 0; w < HISTS; ++w) c += hist[w][threadIdx.x];
+      for (int w = 0; w < HISTS; ++w) {
+        c += hist[w][threadIdx.x];
+        hist[w][threadIdx.x] = 0;
+      }
       own[threadIdx.x] = c;
     }
     if (CL > 1) {
@@ -221,65 +224,104 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
       }
     }
     __syncthreads();
-    prefix |= (uint32_t)digit_s << shift;
+    prefix = prefix << 8 | (uint32_t)digit_s;
     want -= above_s;
     // done at the last digit, or when every key with these digits is kept
     all_ties = bins[digit_s] == want;
-    settled = shift == 0 || all_ties;
+    if (shift == 0 || all_ties) break;
+    shift -= 8;
+#pragma unroll 4
+    for (int i = w0 + lane; i < w1; i += 32) {
+      const uint32_t k = key_of(i) >> shift;
+      if (k >> 8 == prefix) atomicAdd(&mine[k & 255], 1u);
+    }
   }
-  prefix >>= shift;
-  if (CL > 1) cg::this_cluster().sync();  // the last histogram has been read by every CTA
 
   // ---- holes below n and kept rows at or past n, in row order
   const unsigned below = (1u << lane) - 1;
   // first tied key of each warp, where some are not kept
-  unsigned ties_before = 0;
+  unsigned ties = 0;
   if (!all_ties) {
-    unsigned t = 0;
-    for (int i = w0 + lane; i < w1; i += 32) t += key_of(i) >> shift == prefix;
-    ties_before = (unsigned)cluster_prefix<CL>(__reduce_add_sync(0xffffffffu, t), warp_sum, &cta_sum, rank);
+    for (int i = w0 + lane; i < w1; i += 32) ties += key_of(i) >> shift == prefix;
+    ties = (unsigned)cluster_prefix<CL>(__reduce_add_sync(0xffffffffu, ties), warp_sum[0], &cta_sum[0], rank);
   }
-  auto walk = [&](auto &&visit) {
-    unsigned eq = ties_before;
-    for (int i0 = w0; i0 < w1; i0 += 32 * U) {
-      uint32_t k[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + 32 * u + lane;
-        k[u] = i < w1 ? key_of(i) >> shift : 0u;
+  // 32 x 32 rows from c0: lane i has the kept rows of the i-th 32 as bits
+  auto kept_rows = [&](int c0, unsigned &ties_before) -> unsigned {
+    unsigned word = 0;
+    const int rounds = min(32, (w1 - c0 + 31) / 32);
+#pragma unroll 4
+    for (int r = 0; r < rounds; ++r) {
+      const int i = c0 + 32 * r + lane;
+      const uint32_t k = i < w1 ? key_of(i) >> shift : 0u;
+      bool kept = i < w1 && k >= prefix;
+      if (!all_ties) {
+        const bool tied = kept && k == prefix;
+        const unsigned t = __ballot_sync(0xffffffffu, tied);
+        if (tied) kept = ties_before + __popc(t & below) < want;
+        ties_before += __popc(t);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int i = i0 + 32 * u + lane;
-        bool kept = k[u] >= prefix;
-        if (!all_ties) {
-          const unsigned ties = __ballot_sync(0xffffffffu, i < w1 && k[u] == prefix);
-          kept = k[u] > prefix || (k[u] == prefix && eq + __popc(ties & below) < want);
-          eq += __popc(ties);
-        }
-        visit(r0 + i, i < w1, kept);
-      }
+      const unsigned bits = __ballot_sync(0xffffffffu, kept);
+      if (lane == r) word = bits;
     }
+    return word;
   };
-  unsigned holes = 0, tails = 0;
-  walk([&](int row, bool in, bool kept) {
-    holes += in && row < n && !kept;
-    tails += in && row >= n && kept;
-  });
-  holes = __reduce_add_sync(0xffffffffu, holes);
-  tails = __reduce_add_sync(0xffffffffu, tails);
-  const long long first = cluster_prefix<CL>((long long)holes << 32 | tails, warp_sum, &cta_sum, rank);
+  // the bits of `rows` rows from 0
+  auto first_bits = [](long long rows) -> unsigned {
+    return rows <= 0 ? 0u : rows >= 32 ? 0xffffffffu : (1u << rows) - 1;
+  };
+  auto split = [&](int c0, unsigned word, unsigned &hole_bits, unsigned &tail_bits) {
+    const long long row = r0 + (long long)c0 + 32 * lane;
+    const unsigned low = first_bits(n - row);
+    hole_bits = ~word & low & first_bits((long long)r0 + w1 - row);
+    tail_bits = word & ~low;
+  };
+  unsigned word = 0, hole_bits = 0, tail_bits = 0, ties_at = ties;
+  long long found = 0;  // holes and tails of this warp
+  for (int c0 = w0; c0 < w1; c0 += 1024) {
+    word = kept_rows(c0, ties_at);
+    split(c0, word, hole_bits, tail_bits);
+    found += (long long)__reduce_add_sync(0xffffffffu, __popc(hole_bits)) << 32 |
+             __reduce_add_sync(0xffffffffu, __popc(tail_bits));
+  }
+  const long long first = cluster_prefix<CL>(found, warp_sum[1], &cta_sum[1], rank);
+  if (rank == 0 && threadIdx.x == 0) p.new_lens[b] = n;
+  __syncwarp();
+  if (CL > 1) cg::this_cluster().barrier_arrive();  // no CTA's shared memory is read from here on
   unsigned hole = (unsigned)(first >> 32), tail = (unsigned)first;
   int *tail_rows = p.tail + (size_t)b * p.keep;
-  walk([&](int row, bool in, bool kept) {
-    const unsigned h = __ballot_sync(0xffffffffu, in && row < n && !kept), t = __ballot_sync(0xffffffffu, in && row >= n && kept);
+  for (int c0 = w0; c0 < w1; c0 += 1024) {
+    if (w1 - w0 > 1024) {  // else they are there from above
+      word = kept_rows(c0, ties);
+      split(c0, word, hole_bits, tail_bits);
+    }
+    // ranks of each 32 rows' first hole and tail
+    unsigned h = __popc(hole_bits), t = __popc(tail_bits);
+    const unsigned both = t << 16 | h;  // at most 1024 each
+    unsigned incl = both;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    h = hole + ((incl - both) & 0xffff);
+    t = tail + ((incl - both) >> 16);
+    const unsigned total = __shfl_sync(0xffffffffu, incl, 31);
+    hole += total & 0xffff;
+    tail += total >> 16;
     // a hole of rank k is -2 - k for now: move_kernel puts tail_rows[k] there
-    if (in && row < n) index[row] = kept ? row : -2 - (int)(hole + __popc(h & below));
-    if (t >> lane & 1) tail_rows[tail + __popc(t & below)] = row;
-    hole += __popc(h);
-    tail += __popc(t);
-  });
-  if (rank == 0 && threadIdx.x == 0) p.new_lens[b] = n;
+    const int rows = min(n - (r0 + c0), min(1024, w1 - c0));  // rows below n
+    for (int r = 0; 32 * r < rows; ++r) {
+      const unsigned bits = __shfl_sync(0xffffffffu, hole_bits, r), rank0 = __shfl_sync(0xffffffffu, h, r);
+      const int row = r0 + c0 + 32 * r + lane;
+      if (32 * r + lane < rows) index[row] = bits >> lane & 1 ? -2 - (int)(rank0 + __popc(bits & below)) : row;
+    }
+    for (unsigned with = __ballot_sync(0xffffffffu, tail_bits != 0); with; with &= with - 1) {
+      const int r = __ffs(with) - 1;
+      const unsigned bits = __shfl_sync(0xffffffffu, tail_bits, r), rank0 = __shfl_sync(0xffffffffu, t, r);
+      if (bits >> lane & 1) tail_rows[rank0 + __popc(bits & below)] = r0 + c0 + 32 * r + lane;
+    }
+  }
+  if (CL > 1) cg::this_cluster().barrier_wait();
 }
 
 struct MoveParams {

@@ -98,6 +98,15 @@ def test_ties_and_special_scores(g, kind, L):
     check(g, 1, L, L, L // 2, scores=x[None], sink=10, recent=20, inplace=False)
 
 
+@pytest.mark.parametrize("L", [300000, 400000])
+def test_ties_over_many_rows_per_warp(g, L):
+    """More than 1024 rows per warp, some tied ones kept: ranks carry from one 1024 to the next."""
+    rng = np.random.default_rng(L)
+    x = rng.integers(0, 2, (1, L)).astype(float)
+    check(g, 1, L, L, L // 3, scores=x, sink=3, recent=7)
+    check(g, 1, L, L, 3 * L // 4, scores=x, inplace=False)
+
+
 def test_protected_rows_after_earlier_evictions(g):
     """Positions out of order (rows filled holes earlier): protection goes by position, not by place."""
     rng = np.random.default_rng(9)
