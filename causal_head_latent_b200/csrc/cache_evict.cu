@@ -14,11 +14,13 @@
 //     32-bit keys in the order of the rule above (kept in shared memory where they fit);
 //     rounds of 8-bit histograms, summed over the cluster through distributed shared
 //     memory, find the n-th largest key, stopping as soon as all keys with the digits so
-//     far are kept (usually after two or three); ordered scans (a warp owns a contiguous
-//     run of rows and counts by ballots) give every tied row, hole and tail its rank.  No
-//     atomics but the histograms': the result does not depend on order.  Bound by latency
-//     and by what 8 SMs take in: 12 bytes a row (4 without positions).  8 x 131072 rows:
-//     25 us (16 CTAs per sequence: no faster); 32 x 4097: 11.4 us.
+//     far are kept (usually after two or three).  Then a warp turns its contiguous rows into
+//     masks of kept rows, a lane per 32, whose bit counts, summed in order over warps and CTAs,
+//     rank every hole and every row that fills one.  No atomics but the histograms': the result
+//     does not depend on order.  Bound by latency: at this length every first pass through
+//     code costs its instruction fetches, so loops are rolled (unrolled eight times with their
+//     values in registers the same passes took 50 % longer).  8 x 131072 rows: 19 us, of which 5
+//     load and key 12 bytes a row; 32 x 4097: 8 us.
 //  move_kernel    gives each hole the row of its rank, then copies rows, scores and positions, a
 //     warp per row; bound by HBM (elsewhere: 65536 rows of 1 KB in 19 us, 7 TB/s) or by
 //     reading the index (in place).
@@ -52,7 +54,7 @@ struct SelectParams {
   const int *lens;  // may be null
   int *new_lens, *index, *tail;  // [B], [B, keep], [B, keep] scratch
   long long ld;                  // cache_len_max
-  int L, keep, sink, recent, key_cap;
+  int L, keep, sink, recent;
 };
 
 // Exclusive ordered sums over the warps of a cluster: `mine` of each warp (of this CTA and
@@ -80,9 +82,10 @@ __device__ __forceinline__ long long cluster_prefix(long long mine, long long *w
   return before;
 }
 
-template <int CL>
+// CACHED: a CTA's keys fit in its shared memory.
+template <int CL, bool CACHED>
 __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
-  extern __shared__ uint32_t keys[];  // [key_cap]
+  extern __shared__ uint32_t keys[];  // CACHED: [slice]
   __shared__ uint32_t hist[HISTS][256];
   __shared__ uint32_t cta_bins[2][256], bins[256];
   __shared__ long long warp_sum[2][WARPS], cta_sum[2];
@@ -113,7 +116,6 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   const int w0 = min(cnt, warp * wper), w1 = min(cnt, w0 + wper);
 
   // The newest position, with the scores taken along where they fit.
-  const bool cached = cnt <= p.key_cap;
   long long newest = len - 1;
   if (threadIdx.x == 0) newest_s = INT32_MIN;
   for (int i = threadIdx.x; i < HISTS * 256; i += THREADS) (&hist[0][0])[i] = 0;
@@ -127,12 +129,12 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
         const int i = i0 + u * THREADS;
         if (i < cnt) {
           m = max(m, pos[r0 + i]);
-          if (cached) x[u] = score[r0 + i];
+          if (CACHED) x[u] = score[r0 + i];
         }
       }
 #pragma unroll
       for (int u = 0; u < LOADS; ++u)
-        if (cached && i0 + u * THREADS < cnt) keys[i0 + u * THREADS] = __float_as_uint(x[u]);
+        if (CACHED && i0 + u * THREADS < cnt) keys[i0 + u * THREADS] = __float_as_uint(x[u]);
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) atomicMax(&newest_s, m);
@@ -145,11 +147,13 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
       newest = newest_s;
     }
   }
-  auto key_from = [&](long long position, float x) -> uint32_t {
-    return position < p.sink || position > newest - p.recent ? kProtected : ordered(x);
+  const int recent0 = (int)max(newest + 1 - p.recent, (long long)INT32_MIN);  // the first of the recent positions
+  const bool any_recent = p.recent > 0;
+  auto key_from = [&](int position, float x) -> uint32_t {
+    return position < p.sink || (any_recent && position >= recent0) ? kProtected : ordered(x);
   };
   auto key_of = [&](int i) -> uint32_t {
-    return cached ? keys[i] : key_from(pos ? pos[r0 + i] : r0 + i, score[r0 + i]);
+    return CACHED ? keys[i] : key_from(pos ? pos[r0 + i] : r0 + i, score[r0 + i]);
   };
 
   // ---- the n-th largest key, digit by digit: `want` keys with the prefix's digits are still to be kept
@@ -158,26 +162,11 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
   bool all_ties = false;
   uint32_t *mine = hist[warp % HISTS];
   // the first digit, as the keys are made
-  for (int i0 = threadIdx.x; i0 < cnt; i0 += LOADS * THREADS) {
-    int at[LOADS];
-    float x[LOADS];
-#pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-      const int i = i0 + u * THREADS;
-      if (i < cnt) {
-        at[u] = pos ? pos[r0 + i] : r0 + i;
-        x[u] = cached && pos ? __uint_as_float(keys[i]) : score[r0 + i];
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < LOADS; ++u) {
-      const int i = i0 + u * THREADS;
-      if (i < cnt) {
-        const uint32_t k = key_from(at[u], x[u]);
-        if (cached) keys[i] = k;
-        atomicAdd(&mine[k >> 24], 1u);
-      }
-    }
+#pragma unroll 4
+  for (int i = threadIdx.x; i < cnt; i += THREADS) {
+    const uint32_t k = key_from(pos ? pos[r0 + i] : r0 + i, CACHED && pos ? __uint_as_float(keys[i]) : score[r0 + i]);
+    if (CACHED) keys[i] = k;
+    atomicAdd(&mine[k >> 24], 1u);
   }
   while (true) {
     __syncthreads();
@@ -239,29 +228,35 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
 
   // ---- holes below n and kept rows at or past n, in row order
   const unsigned below = (1u << lane) - 1;
-  // first tied key of each warp, where some are not kept
+  // the least key kept: all with its digits, or (shift 0) the first `want` of those equal to it
+  const uint32_t least = prefix << shift;
   unsigned ties = 0;
   if (!all_ties) {
-    for (int i = w0 + lane; i < w1; i += 32) ties += key_of(i) >> shift == prefix;
+    for (int i = w0 + lane; i < w1; i += 32) ties += key_of(i) == least;
     ties = (unsigned)cluster_prefix<CL>(__reduce_add_sync(0xffffffffu, ties), warp_sum[0], &cta_sum[0], rank);
   }
   // 32 x 32 rows from c0: lane i has the kept rows of the i-th 32 as bits
   auto kept_rows = [&](int c0, unsigned &ties_before) -> unsigned {
     unsigned word = 0;
     const int rounds = min(32, (w1 - c0 + 31) / 32);
+    if (all_ties) {
 #pragma unroll 4
-    for (int r = 0; r < rounds; ++r) {
-      const int i = c0 + 32 * r + lane;
-      const uint32_t k = i < w1 ? key_of(i) >> shift : 0u;
-      bool kept = i < w1 && k >= prefix;
-      if (!all_ties) {
-        const bool tied = kept && k == prefix;
-        const unsigned t = __ballot_sync(0xffffffffu, tied);
-        if (tied) kept = ties_before + __popc(t & below) < want;
-        ties_before += __popc(t);
+      for (int r = 0; r < rounds; ++r) {
+        const int i = c0 + 32 * r + lane;
+        const unsigned bits = __ballot_sync(0xffffffffu, i < w1 && key_of(i) >= least);
+        if (lane == r) word = bits;
       }
-      const unsigned bits = __ballot_sync(0xffffffffu, kept);
-      if (lane == r) word = bits;
+    } else {
+      for (int r = 0; r < rounds; ++r) {
+        const int i = c0 + 32 * r + lane;
+        const uint32_t k = i < w1 ? key_of(i) : 0u;
+        const bool tied = i < w1 && k == least;
+        const unsigned t = __ballot_sync(0xffffffffu, tied);
+        const bool kept = tied ? ties_before + __popc(t & below) < want : i < w1 && k > least;
+        ties_before += __popc(t);
+        const unsigned bits = __ballot_sync(0xffffffffu, kept);
+        if (lane == r) word = bits;
+      }
     }
     return word;
   };
@@ -315,11 +310,8 @@ __global__ void __launch_bounds__(THREADS) select_kernel(const SelectParams p) {
       const int row = r0 + c0 + 32 * r + lane;
       if (32 * r + lane < rows) index[row] = bits >> lane & 1 ? -2 - (int)(rank0 + __popc(bits & below)) : row;
     }
-    for (unsigned with = __ballot_sync(0xffffffffu, tail_bits != 0); with; with &= with - 1) {
-      const int r = __ffs(with) - 1;
-      const unsigned bits = __shfl_sync(0xffffffffu, tail_bits, r), rank0 = __shfl_sync(0xffffffffu, t, r);
-      if (bits >> lane & 1) tail_rows[rank0 + __popc(bits & below)] = r0 + c0 + 32 * r + lane;
-    }
+    for (; tail_bits; tail_bits &= tail_bits - 1) tail_rows[t++] = r0 + c0 + 32 * lane + __ffs(tail_bits) - 1;
+    __syncwarp();
   }
   if (CL > 1) cg::this_cluster().barrier_wait();
 }
@@ -397,10 +389,9 @@ __global__ void __launch_bounds__(MT) move_kernel(const MoveParams p) {
 constexpr int kKeyCap = 40960;         // keys a CTA may hold in shared memory (160 KB)
 constexpr int kOneCtaRows = 8192;      // up to here one CTA per sequence: no cluster barriers
 
-template <int CL>
-static int launch_select(const SelectParams &p, int B, SmemSlot slot, cudaStream_t stream) {
-  const size_t smem = (size_t)p.key_cap * 4;
-  if (!set_smem_limit_once(reinterpret_cast<const void *>(select_kernel<CL>), kKeyCap * 4, slot)) return -1;
+template <int CL, bool CACHED>
+static int launch_select(const SelectParams &p, int B, size_t smem, SmemSlot slot, cudaStream_t stream) {
+  if (CACHED && !set_smem_limit_once(reinterpret_cast<const void *>(select_kernel<CL, CACHED>), kKeyCap * 4, slot)) return -1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)B * CL);
   cfg.blockDim = dim3(THREADS);
@@ -412,7 +403,7 @@ static int launch_select(const SelectParams &p, int B, SmemSlot slot, cudaStream
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, select_kernel<CL>, p) == cudaSuccess ? 0 : -1;
+  return cudaLaunchKernelEx(&cfg, select_kernel<CL, CACHED>, p) == cudaSuccess ? 0 : -1;
 }
 
 }  // namespace cache_evict
@@ -434,9 +425,11 @@ int launch_cache_evict(const EvictArgs &a, cudaStream_t stream) {
   s.recent = a.recent;
   const bool one = a.L <= kOneCtaRows;
   const long long per = one ? a.L : (((long long)a.L + 7) / 8 + 31) / 32 * 32;
-  s.key_cap = (int)(per <= kKeyCap ? per : 0);  // longer slices read their scores again in every pass
-  if ((one ? launch_select<1>(s, a.B, kSmemEvict1, stream) : launch_select<8>(s, a.B, kSmemEvict8, stream)) != 0)
-    return -1;
+  // longer slices read their scores again in every pass
+  const int rc = one ? launch_select<1, true>(s, a.B, per * 4, kSmemEvict1, stream)
+                 : per <= kKeyCap ? launch_select<8, true>(s, a.B, per * 4, kSmemEvict8, stream)
+                                  : launch_select<8, false>(s, a.B, 0, kSmemEvict8, stream);
+  if (rc != 0) return -1;
   MoveParams m;
   for (int i = 0; i < 2; ++i) m.rows[i] = a.rows[i];
   m.score = a.score;
