@@ -408,6 +408,17 @@ def _shape(t, name, dims):
     return t.shape
 
 
+def _workspace(t, dev):
+    """Address and bytes of a contiguous workspace on device `dev` (None for none)."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev:
+        raise ValueError("workspace must live on the current CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
@@ -463,7 +474,7 @@ def gmla_attend_decode_fp4(Q, codes, scales, L, W_k, W_v, O, num_heads, cache_sc
     dev = torch.cuda.current_device()
     B, Lmax, half = _shape(codes, "codes", 3)
     d, d_c, bf16, H = _shape(Q, "Q", 2)[1], 2 * half, torch.bfloat16, int(num_heads)
-    wp, wb = _ws(workspace)
+    wp, wb = _workspace(workspace, dev)
     code = lib.gmla_attend_decode_fp4(
         _tensor(Q, "Q", bf16, (B, d), dev), _tensor(codes, "codes", torch.uint8, (B, Lmax, half), dev),
         _tensor(scales, "scales", torch.uint8, (B, Lmax, half // 8), dev), float(cache_scale), B, Lmax, int(L),
@@ -485,7 +496,7 @@ def gmla_cache_score(Q, C, L, W_k, score, num_heads, lens=None, scale=0.0, decay
     dev = torch.cuda.current_device()
     B, Lmax, d_c = _shape(C, "C", 3)
     d, bf16, H = _shape(Q, "Q", 2)[1], torch.bfloat16, int(num_heads)
-    wp, wb = _ws(workspace)
+    wp, wb = _workspace(workspace, dev)
     code = lib.gmla_cache_score(
         _tensor(Q, "Q", bf16, (B, d), dev), _tensor(C, "C", bf16, (B, Lmax, d_c), dev), B, Lmax, int(L),
         _tensor(lens, "lens", torch.int32, (B,), dev), H, _head_width(d, H), d_c,
@@ -522,7 +533,7 @@ def gmla_cache_evict(rows, score, L, keep, index, new_lens, pos=None, lens=None,
                    _tensor(t, "dst", r.dtype, (B, Dmax, w), dev)]
     if len(rows) == 1:
         arrays += [None, 0, None]
-    wp, wb = _ws(workspace)
+    wp, wb = _workspace(workspace, dev)
     code = lib.gmla_cache_evict(
         *arrays, _tensor(score, "score", torch.float32, (B, Lmax), dev),
         _tensor(dst_score, "dst_score", torch.float32, (B, Dmax), dev), _tensor(pos, "pos", torch.int32, (B, Lmax), dev),

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(MAX_THREADS) quantize_kernel(const Fp4StoreArg
         x[2 * i] = __uint_as_float(w[4 * j + i] << 16);
         x[2 * i + 1] = __uint_as_float(w[4 * j + i] & 0xffff0000u);
         // to a multiple of 2^-12: half-way points are multiples of 1/4, and other quotients are 2^-10 or more from them
-        scale_round2(x[2 * i], x[2 * i + 1], inv, 3072.f);
+        scale_round2(x[2 * i], x[2 * i + 1], inv, 0x1.8p11f);
       }
       code[j] = f32x8_to_fp4(x);
       // a magnitude that rounds to zero is held as +0

@@ -157,3 +157,21 @@ def test_binding_refuses(g, monkeypatch):
         g.gmla_cache_evict([C], torch.zeros(2, 4), 4, 2, None, None, dst_score=torch.zeros(2, 4))
     with pytest.raises(ValueError, match="must match"):
         g.gmla_cache_evict([C], torch.zeros(2, 4), 4, 2, None, None, dst=[C])
+
+
+def test_binding_refuses_workspaces(g, monkeypatch):
+    """A workspace elsewhere would be written through by the kernels."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    Q, C, W = (torch.zeros(*s, dtype=torch.bfloat16) for s in ((2, 128), (2, 9, 128), (128, 128)))
+    codes, scales = (torch.zeros(2, 9, w, dtype=torch.uint8) for w in (64, 8))
+    score, index, lens = torch.zeros(2, 9), torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: g.gmla_attend_decode_fp4(Q, codes, scales, 9, W, W, Q, 1, workspace=ws),
+                 lambda: g.gmla_cache_score(Q, C, 9, W, score, 1, workspace=ws)):
+        with pytest.raises(ValueError, match="workspace must live"):
+            call()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # the device of tensors on the CPU, as far as the checks go
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        g.gmla_cache_evict([C], score, 9, 4, index, lens, workspace=ws[::2])
+    monkeypatch.undo()
+    assert g._workspace(None, 0) == (None, 0) and g._workspace(ws, -1) == (ws.data_ptr(), 1 << 16)
