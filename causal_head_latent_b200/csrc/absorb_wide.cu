@@ -5,9 +5,9 @@
 // how much of the float32 result is kept:
 //   float16        11 bits, for products with 4-bit rows (which are exact in
 //                  float16); |q~| saturates at 65504
-//   bfloat16 pair  hi = bf16(q~), lo = bf16(q~ - hi): about 16 bits, for the
-//                  accumulated attention weights, whose float32 sums should not
-//                  carry an 8-bit rounding of the query
+//   bfloat16 parts hi = bf16(q~), lo = bf16(q~ - hi), for the accumulated attention
+//                  weights, whose float32 sums should not carry an 8-bit rounding of
+//                  the query: 17 bits; with few heads also third = bf16(q~ - hi - lo): 24
 // One CTA per (head, 128 latent columns, 32 sequences): D[c, b] = A B with A =
 // 128 columns of W_k^(h) read MN-major, B = the 32 query rows (K-major), K = 128.
 // Bound by latency: each CTA reads 32 KB of W_k once.
@@ -34,7 +34,7 @@ struct Smem {
 static_assert(sizeof(Smem) + 1024 <= 48 * 1024, "fits the default shared-memory limit");
 
 struct Params {
-  uint16_t *f16, *hi, *lo;
+  uint16_t *f16, *hi, *lo, *third;
   int B, H, dc;
   float s;
   unsigned *status;
@@ -96,8 +96,11 @@ __global__ void __launch_bounds__(THREADS)
           p.f16[i] = __half_as_ushort(__float2half_rn(x != x ? x : fminf(fmaxf(x, -65504.f), 65504.f)));
         } else {
           const __nv_bfloat16 hi = __float2bfloat16_rn(x);
+          const float rest = x - __bfloat162float(hi);
+          const __nv_bfloat16 lo = __float2bfloat16_rn(rest);
           p.hi[i] = __bfloat16_as_ushort(hi);
-          p.lo[i] = __bfloat16_as_ushort(__float2bfloat16_rn(x - __bfloat162float(hi)));
+          p.lo[i] = __bfloat16_as_ushort(lo);
+          if (p.third) p.third[i] = __bfloat16_as_ushort(__float2bfloat16_rn(rest - __bfloat162float(lo)));
         }
       }
     }
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(THREADS)
 }  // namespace absorb_wide
 
 int launch_absorb_wide(const uint16_t *Q, const uint16_t *Wk, int B, int H, int dc, float s, uint16_t *f16,
-                       uint16_t *hi, uint16_t *lo, unsigned *status, cudaStream_t stream) {
+                       uint16_t *hi, uint16_t *lo, uint16_t *third, unsigned *status, cudaStream_t stream) {
   using namespace absorb_wide;
   CUtensorMap tw, tq;
   const long long dw[2] = {dc, (long long)H * HD}, sw[1] = {dc};
@@ -122,7 +125,7 @@ int launch_absorb_wide(const uint16_t *Q, const uint16_t *Wk, int B, int H, int 
   const long long dq[2] = {(long long)H * HD, B}, sq[1] = {(long long)H * HD};
   const unsigned bq[2] = {64, NB};
   if (!make_tmap_bf16(&tw, Wk, 2, dw, sw, bw) || !make_tmap_bf16(&tq, Q, 2, dq, sq, bq)) return -1;
-  const Params p{f16, hi, lo, B, H, dc, s, status};
+  const Params p{f16, hi, lo, third, B, H, dc, s, status};
   absorb_wide_kernel<<<dim3(H, (dc + 127) / 128, (B + NB - 1) / NB), THREADS, sizeof(Smem) + 1024, stream>>>(tw, tq, p);
   return cudaGetLastError() == cudaSuccess ? 0 : -1;
 }

@@ -580,7 +580,7 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
   const long long G = share_count(a.B, a.L, KT, kFp4PieceTiles);
   constexpr float kLog2e = 1.4426950408889634f;
   if (!set_smem_limit_once(reinterpret_cast<const void *>(decode_kernel), (int)smem_bytes(), kSmemLatentFp4)) return -1;
-  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e * a.cache_scale, qt, nullptr, nullptr, a.status,
+  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e * a.cache_scale, qt, nullptr, nullptr, nullptr, a.status,
                          stream) != 0)
     return -1;
   CUtensorMap tq;

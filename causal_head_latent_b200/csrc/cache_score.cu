@@ -2,9 +2,13 @@
 //   score[b, s] = decay * score[b, s] + sum_h a_bhs,   a_bh = softmax_s(q~_bh . c_bs),
 // for one new query per sequence over the bfloat16 latent cache, with q~ the absorbed
 // query (log2(e) / sqrt(D) folded in).  The sum runs over steps in float32, so one step's
-// weights should not carry bfloat16's 8 bits: q~ goes in as hi + lo (about 16 bits) and
-//   S = hi C^T + lo C^T
-// on tcgen05 tensor cores, float32 accumulators; the rows c are bfloat16 as they are.
+// weights should not carry bfloat16's 8 bits: q~ goes in as parts, and
+//   S = hi C^T + lo C^T (+ third C^T)
+// on tcgen05 tensor cores, float32 accumulators; the rows c are bfloat16 as they are.  Two
+// kinds of errors matter: what two parts leave (17 bits), and the accumulators' rounding,
+// which grows with the MMAs that add to a sum of full size (64 a tile at d_c = 512).  Both
+// average out over heads: at 96 heads they are 7e-7 relative in all, at one head 4e-6.  So
+// up to 64 heads (FEW) q~ has a third part, and lo and third add up in an accumulator of their own.
 //
 // Two launches per group of sequences.
 //  scores_kernel   S of every (head, row), stored as float32, and per piece the running
@@ -23,8 +27,13 @@
 // leave 32 KB for the rows; so the ring holds eight 16 KB chunks, a whole tile).
 //   warp 0       TMA of the rows, 64-column chunks
 //   warp 1       TMEM owner; issues the MMAs (converged, one lane predicated)
-//   warp 2       TMA of q~ hi
-//   warps 4..7   q~ lo into TMEM; per tile the running softmax state and the store of S
+//   warp 2       TMA of q~ hi (and lo)
+//   warps 4..7   q~ lo (FEW: third) into TMEM; per tile the running softmax state and the store of S
+// FEW: rows 0..63 of the A tile are hi and rows 64..127 lo, in shared memory (128 KB, so five
+// slots are left); third is in tensor memory, lanes 64..127, over zeros: as many MMAs as
+// above.  The warps of lanes 64..127 hand their sums to those of the heads through shared memory.
+// Up to 32 heads the second half of hi's chunks stands 32 rows lower, so that it adds up in
+// lanes 32..63, and those are handed over too (one head, d_c = 512: 1.4e-6 to 6e-7).
 // TMEM: D buffers at columns 0 and 128, q~ lo at 256 (a column holds two elements).
 #include <math.h>
 
@@ -41,29 +50,45 @@ constexpr int HMAX = 96;
 constexpr int KT = kScoreTileKeys;
 constexpr int NUM_THREADS = 256;
 constexpr int NCHUNK = 8;                   // 64-wide d_c chunks (d_c <= 512)
-constexpr int QCHUNK = HMAX * 128;          // rows 96..127 of a 128-row A tile alias what follows: S rows nobody reads
-constexpr int Q_BYTES = NCHUNK * QCHUNK;
 constexpr int CCHUNK = KT * 128;            // 128 rows x 64 columns
-constexpr int NSLOT = 8;
 constexpr int TM_D = 0, TM_LO = 256;
 constexpr unsigned long long kDrainLimitNs = 100000000ull;
-static_assert(CCHUNK >= 32 * 128, "the first ring slot covers the q~ tail");
+
+// Shared memory for up to kScoreFewHeads heads (FEW) and for more.
+template <bool FEW>
+struct Plan {
+  static constexpr int ROWS = FEW ? kScoreFewHeads : HMAX;  // per part
+  static constexpr int QCHUNK = (FEW ? 2 : 1) * ROWS * 128;
+  static constexpr int Q_BYTES = NCHUNK * QCHUNK;
+  static constexpr int NSLOT = FEW ? 5 : 8;
+  static constexpr int HAND_BYTES = FEW ? 2 * 2 * 32 * 128 : 0;  // two buffers of 32 sums per lane for two warps
+  // !FEW: rows 96..127 of a 128-row A tile alias what follows: S rows nobody reads
+  static_assert(QCHUNK >= 128 * 128 || NSLOT * CCHUNK >= 32 * 128, "the ring covers the q~ tail");
+  static constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + HAND_BYTES + 8 * (2 * NSLOT + 8) + 20; }
+};
+static_assert(Plan<true>::smem_bytes() <= 232448 && Plan<false>::smem_bytes() <= 232448,
+              "dynamic shared memory above the 227 KB a CTA may have");
+static_assert(kScoreFewHeads == 64, "two warps of heads, two of the lanes 64 above them");
 
 struct Params {
   int H, dc, Hp;            // Hp: heads rounded up to 32
   long long tiles_max;      // tiles of a sequence in S
   ShareBatch batch;
-  const uint16_t *lo;       // [B, H, dc]
+  const uint16_t *last;     // the part in tensor memory (lo; FEW: third) [B, H, dc]
   float *part_m, *part_l;   // [R, H]
   float *S;                 // [B][tiles_max][KT / 4][Hp][4]
   unsigned *status;
 };
 
+template <bool FEW>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    scores_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC, const Params p) {
+    scores_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmT,
+                  const __grid_constant__ CUtensorMap tmC, const Params p) {
+  constexpr int QCHUNK = Plan<FEW>::QCHUNK, Q_BYTES = Plan<FEW>::Q_BYTES, NSLOT = Plan<FEW>::NSLOT;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t *sq = smem, *sc = sq + Q_BYTES;
-  uint64_t *full = reinterpret_cast<uint64_t *>(sc + NSLOT * CCHUNK);  // [NSLOT]
+  float4 *hand = reinterpret_cast<float4 *>(sc + NSLOT * CCHUNK);      // [2][2][8][32]
+  uint64_t *full = reinterpret_cast<uint64_t *>(sc + NSLOT * CCHUNK + Plan<FEW>::HAND_BYTES);  // [NSLOT]
   uint64_t *empty = full + NSLOT;                                      // [NSLOT]
   uint64_t *d_full = empty + NSLOT;                                    // [2]
   uint64_t *d_free = d_full + 2;                                       // [2]
@@ -151,9 +176,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int j = 0; ok && j < pc.n; ++j, ++g) {
         if (g >= 2) ok = warp_wait_relaxed(&d_free[g & 1], ((g - 2) >> 1) & 1, p.status);
         const uint32_t d = tmem + TM_D + (g & 1) * 128;
-        // A piece's first tile takes its hi products first, while lo is on its way to TMEM (the ring
-        // holds a whole tile); the others take both per chunk.
-        const int rounds = j == 0 ? 2 : 1;
+        // A piece's first tile takes the products of shared memory first, while the last part is on its way
+        // to TMEM, if the ring holds the whole tile; the others take both per chunk.
+        const int rounds = j == 0 && nchunk <= NSLOT ? 2 : 1;
         for (int r = 0; ok && r < rounds; ++r) {
           const bool do_hi = r == 0, do_lo = r == rounds - 1;
           if (j == 0 && do_lo) ok = warp_wait(lo_full, i & 1, p.status);
@@ -185,11 +210,16 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   } else if (warp == 2) {
     if (lane == 0) {
       tma_prefetch_desc(&tmQ);
-      grid_dependency_wait();  // q~ hi
+      if (FEW) tma_prefetch_desc(&tmT);
+      grid_dependency_wait();  // q~
       for (int i = 0; walk.next(batch, &pc); ++i) {
         if (i > 0 && !mbar_wait(q_free, (i - 1) & 1, p.status)) break;
         mbar_arrive_expect_tx(q_full, nchunk * QCHUNK);
-        for (int kc = 0; kc < nchunk; ++kc) tma_load_3d(sq + kc * QCHUNK, &tmQ, q_full, kc * 64, 0, pc.b);
+        for (int kc = 0; kc < nchunk; ++kc) {
+          // rows before the first are zeros
+          tma_load_3d(sq + kc * QCHUNK, &tmQ, q_full, kc * 64, FEW && p.H <= 32 && 2 * kc >= nchunk ? -32 : 0, pc.b);
+          if (FEW) tma_load_3d(sq + kc * QCHUNK + QCHUNK / 2, &tmT, q_full, kc * 64, 0, pc.b);
+        }
         if (!mbar_wait_limit(q_full, i & 1, p.status, kDrainLimitNs)) break;
       }
     }
@@ -197,12 +227,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------------ softmax state, S
     const int quarter = warp & 3, h = quarter * 32 + lane;  // TMEM lane = head
     const bool head_ok = h < p.H;
+    // The lanes of this warp are heads or (FEW) what is added to a head: the warps that hand over use
+    // a barrier and a buffer each, the warp of a head reads one or (up to 32 heads) two.
+    const bool halves = FEW && p.H <= 32;
+    const bool in_use = halves ? quarter < 3 : (FEW ? quarter & 1 : quarter) * 32 < p.H;
+    const int bar = halves ? 1 : 1 + (quarter & 1), bar_threads = halves ? 96 : 64;
+    const bool gives = halves ? quarter > 0 : quarter >= 2;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     bool ok = true;
     for (int i = 0, g = 0; ok && walk.next(batch, &pc); ++i) {
       if (i == 0) grid_dependency_wait();
-      // q~ lo of the piece (the MMAs of the piece before are done: its last d_full was waited for)
-      const uint4 *src = reinterpret_cast<const uint4 *>(p.lo + ((size_t)pc.b * p.H + (head_ok ? h : 0)) * p.dc);
+      // The last part of q~ of the piece (the MMAs of the piece before are done: its last d_full was waited for).
+      const int hq = FEW ? h - 64 : h;
+      const bool q_ok = hq >= 0 && hq < p.H;
+      const uint4 *src = reinterpret_cast<const uint4 *>(p.last + ((size_t)pc.b * p.H + (q_ok ? hq : 0)) * p.dc);
 #pragma unroll 1
       for (int k0 = 0; k0 < nchunk; k0 += 4) {  // four chunks' loads in flight
         uint4 w[4][8];
@@ -210,7 +248,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            w[c][k] = head_ok && k0 + c < nchunk ? src[(k0 + c) * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
+            w[c][k] = q_ok && k0 + c < nchunk ? src[(k0 + c) * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v[32];
@@ -230,6 +268,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < pc.n; ++j, ++g) {
         ok = warp_wait(&d_full[g & 1], (g >> 1) & 1, p.status);
+        if (FEW && in_use) ok = !bar_or(bar, bar_threads, !ok);  // all warps of a head go on or all leave
         if (!ok) break;
         tc_fence_after();
         const int left = pc.len - (pc.tile0 + j) * KT;  // visible rows of this tile
@@ -238,11 +277,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll 1
         for (int c0 = 0; c0 < KT; c0 += 32) {
           float x[32];
-          if (quarter * 32 < p.H) tmem_ld32(tmem + lane_off + TM_D + (g & 1) * 128 + c0, x);
+          if (in_use) tmem_ld32(tmem + lane_off + TM_D + (g & 1) * 128 + c0, x);
           if (c0 + 32 == KT) {  // the last read of this D buffer
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&d_free[g & 1]);
+          }
+          if (FEW && in_use) {  // two buffers by turns: the one before last was read before this barrier's last turn
+            float4 *buf = hand + ((c0 / 32 & 1) * 2 + (quarter & 1)) * 256 + lane;
+            if (gives)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) buf[32 * k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+            bar_sync(bar, bar_threads);
+            for (int from = 0; !gives && from < (halves ? 2 : 1); ++from)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 v = buf[256 * from + 32 * k];
+                x[4 * k] += v.x;
+                x[4 * k + 1] += v.y;
+                x[4 * k + 2] += v.z;
+                x[4 * k + 3] += v.w;
+              }
           }
           if (head_ok && left > c0) {
 #pragma unroll
@@ -285,9 +340,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tmem_dealloc(tmem, 512);
   }
 }
-
-constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + 8 * (2 * NSLOT + 8) + 20; }
-static_assert(smem_bytes() <= 232448, "dynamic shared memory above the 227 KB a CTA may have");
 
 // Each head's log-sum-exp from the states of a sequence's pieces, by `threads` threads of a
 // block, several per head; the records in a fixed order.  lse: shared or global memory.
@@ -426,24 +478,28 @@ __global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
 
 }  // namespace cache_score
 
-int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
+template <bool FEW>
+static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t stream) {
   using namespace cache_score;
+  constexpr size_t smem = Plan<FEW>::smem_bytes();
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   const ScoreLayout lay = score_layout(reinterpret_cast<uintptr_t>(ws), a.B, a.L, a.H, a.dc);
-  uint16_t *hi = reinterpret_cast<uint16_t *>(ws + lay.hi), *lo = reinterpret_cast<uint16_t *>(ws + lay.lo);
+  uint16_t *hi = reinterpret_cast<uint16_t *>(ws + lay.hi), *lo = reinterpret_cast<uint16_t *>(ws + lay.lo),
+           *third = FEW ? reinterpret_cast<uint16_t *>(ws + lay.third) : nullptr;
   constexpr float kLog2e = 1.4426950408889634f;
-  if (!set_smem_limit_once(reinterpret_cast<const void *>(scores_kernel), (int)smem_bytes(), kSmemScore)) return -1;
-  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e, nullptr, hi, lo, a.status, stream) != 0)
+  if (!set_smem_limit_once(reinterpret_cast<const void *>(scores_kernel<FEW>), (int)smem, slot)) return -1;
+  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e, nullptr, hi, lo, third, a.status, stream) != 0)
     return -1;
   const int group = (int)score_group(a.B, a.L, a.H);
   for (int b0 = 0; b0 < a.B; b0 += group) {
     const int nb = a.B - b0 < group ? a.B - b0 : group;
-    CUtensorMap tq, tc;
+    CUtensorMap tq, tt, tc;
     const long long dq[3] = {a.dc, a.H, nb}, sq[2] = {a.dc, (long long)a.H * a.dc};
-    const unsigned bq[3] = {64, HMAX, 1};
+    const unsigned bq[3] = {64, Plan<FEW>::ROWS, 1};
     const long long dcm[3] = {a.dc, a.L, nb}, scm[2] = {a.dc, a.cache_len_max * a.dc};
     const unsigned bc[3] = {64, KT, 1};
     if (!make_tmap_bf16(&tq, hi + (size_t)b0 * a.H * a.dc, 3, dq, sq, bq) ||
+        !make_tmap_bf16(&tt, lo + (size_t)b0 * a.H * a.dc, 3, dq, sq, bq) ||
         !make_tmap_bf16(&tc, a.C + (size_t)b0 * a.cache_len_max * a.dc, 3, dcm, scm, bc))
       return -1;
     Params p;
@@ -452,7 +508,7 @@ int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
     p.Hp = (int)score_heads(a.H);
     p.tiles_max = score_tiles(a.L);
     p.batch = ShareBatch{a.lens ? a.lens + b0 : nullptr, nb, a.L, KT, kScorePieceTiles};
-    p.lo = lo + (size_t)b0 * a.H * a.dc;
+    p.last = (FEW ? third : lo) + (size_t)b0 * a.H * a.dc;
     p.part_m = reinterpret_cast<float *>(ws + lay.pm);
     p.part_l = reinterpret_cast<float *>(ws + lay.pl);
     p.S = reinterpret_cast<float *>(ws + lay.s);
@@ -461,7 +517,7 @@ int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
     // Beginning beside a short launch hides 2 us (the sums at B=1, L=1001: 24.6 against 26.7); beside a
     // long one it takes from its bandwidth (B=32, L=131072: 1.49 ms against 1.39).
     const bool beside = p.tiles_max * nb <= 8 * kShares;
-    if (launch_beside(beside && b0 == 0, scores_kernel, dim3((unsigned)G), dim3(NUM_THREADS), smem_bytes(), stream, tq, tc,
+    if (launch_beside(beside && b0 == 0, scores_kernel<FEW>, dim3((unsigned)G), dim3(NUM_THREADS), smem, stream, tq, tt, tc,
                       p) != 0)
       return -1;
     SumParams u;
@@ -488,6 +544,11 @@ int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
       return -1;
   }
   return 0;
+}
+
+int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
+  return a.H <= kScoreFewHeads ? launch_cache_score<true>(a, kSmemScoreFew, stream)
+                               : launch_cache_score<false>(a, kSmemScore, stream);
 }
 
 }  // namespace gmla

@@ -84,9 +84,12 @@ inline long long score_group(long long B, long long L, long long H) {
   return n < 1 ? 1 : n > B ? B : n;
 }
 
-// q~ as bfloat16 hi and lo [B,H,dc] | of a group: m, l float [R,H], log-sum-exp float [n,H], scores.
+// Up to this many heads q~ has a third part.
+constexpr int kScoreFewHeads = 64;
+
+// q~ as bfloat16 hi, lo (and third) [B,H,dc] | of a group: m, l float [R,H], log-sum-exp float [n,H], scores.
 struct ScoreLayout {
-  size_t hi, lo, pm, pl, lse, s, end;
+  size_t hi, lo, third, pm, pl, lse, s, end;
 };
 inline ScoreLayout score_layout(uintptr_t base, long long B, long long L, long long H, long long dc) {
   const long long n = score_group(B, L, H);
@@ -97,6 +100,8 @@ inline ScoreLayout score_layout(uintptr_t base, long long B, long long L, long l
   off += ws_round(2 * (size_t)B * H * dc);
   o.lo = off;
   off += ws_round(2 * (size_t)B * H * dc);
+  o.third = off;
+  if (H <= kScoreFewHeads) off += ws_round(2 * (size_t)B * H * dc);
   o.pm = off;
   off += ws_round(4 * R * H);
   o.pl = off;

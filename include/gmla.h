@@ -506,8 +506,8 @@ GMLA_API size_t gmla_attend_decode_fp4_workspace_size(int64_t B, int64_t L, int6
  *     score[b, s] = decay * score[b, s] + sum_h a_bhs
  * with a_bhs the softmax weights of gmla_attend_decode (rows of every head sum
  * to 1, so a call adds H to the scores of a sequence).  What gmla_cache_evict
- * goes by.  Float32 throughout: the absorbed query is carried with about 16 bits
- * (two bfloat16 parts), the cache rows as they are.
+ * goes by.  Float32 throughout: the absorbed query is carried with 17 bits (two
+ * bfloat16 parts), up to 64 heads with 24 (three), the cache rows as they are.
  *
  *  Q, C, W_k, scale  as gmla_attend_decode
  *  L, lens  as gmla_attend_decode_fp4 (lens: optional DEVICE int32 array).  Scores of

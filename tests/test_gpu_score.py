@@ -134,3 +134,26 @@ def test_no_decay_overwrites_what_nobody_initialised(g):
     add = plain(f64(Q), f64(C), [150, 150], f64(W_k), 4)
     assert np.linalg.norm(f64(score)[:, :150] - add[:, :150]) <= REL * np.linalg.norm(add)
     assert torch.isnan(score[:, 150:]).all()
+
+
+@pytest.mark.parametrize("H,d_c", [(1, 512), (1, 64), (7, 320), (16, 512), (31, 448), (32, 512), (33, 512), (48, 192),
+                                   (63, 512), (64, 512), (64, 384)])
+@pytest.mark.parametrize("B,L", [(1, 4100), (5, 700)])
+def test_few_heads_keep_the_whole_query(g, H, d_c, B, L):
+    """With few heads nothing averages out, so q~ has 24 bits and its parts' sums are kept apart.
+
+    Left are the accumulators: each of the d_c / 16 additions to hi's sum (half of them up to 32 heads) truncates it,
+    by half a step (2^-22 where the sum is between 2 and 4, as for the rows that weigh most) on average, all of one
+    sign; a weight moves by ln 2 times that."""
+    rng = np.random.default_rng(H + d_c + L)
+    C, Q = rand(rng, B, L, d_c), rand(rng, B, H * 128)
+    W_k = rand(rng, H * 128, d_c) * d_c ** -0.5
+    score = torch.empty(B, L, device="cuda")
+    lens = [L - 37 * b for b in range(B)]
+    dl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    ws = torch.full((g.gmla_cache_score_workspace_size(B, L, H, d_c),), 0xFF, dtype=torch.uint8, device="cuda")
+    g.gmla_cache_score(Q, C, L, W_k, score, H, lens=dl, decay=0.0, workspace=ws)
+    want, got = plain(f64(Q), f64(C), lens, f64(W_k), H), f64(score)
+    adds = max(16, d_c // 16) // (2 if H <= 32 else 1)  # at least 16: float32 itself leaves 16 * 2^-24
+    for b, n in enumerate(lens):
+        assert np.linalg.norm(got[b, :n] - want[b, :n]) <= adds * 2.0 ** -22 * np.log(2) * np.linalg.norm(want[b, :n])
