@@ -519,28 +519,29 @@ def gmla_cache_evict(rows, score, L, keep, index, new_lens, pos=None, lens=None,
     B, Lmax = _shape(score, "score", 2)
     if not 1 <= len(rows) <= 2:
         raise ValueError("rows must hold one or two tensors")
-    if dst is None:
+    in_place = dst is None
+    if in_place:
         if dst_score is not None or dst_pos is not None:
             raise ValueError("dst_score and dst_pos go with dst")
-        dst, dst_score, dst_pos = rows, score, pos
     elif len(dst) != len(rows) or dst_score is None or (dst_pos is None) != (pos is None):
         raise ValueError("dst, dst_score and dst_pos must match rows, score and pos")
-    Dmax = _shape(dst_score, "dst_score", 2)[1]
+    Dmax = Lmax if in_place else _shape(dst_score, "dst_score", 2)[1]
     arrays = []
-    for r, t in zip(rows, dst):
-        w = _shape(r, "rows", 3)[2]
-        arrays += [_tensor(r, "rows", r.dtype, (B, Lmax, w), dev), w * r.element_size(),
-                   _tensor(t, "dst", r.dtype, (B, Dmax, w), dev)]
+    for i, r in enumerate(rows):
+        dtype, w = r.dtype, _shape(r, "rows", 3)[2]
+        src = _tensor(r, "rows", dtype, (B, Lmax, w), dev)
+        arrays += [src, w * r.element_size(), src if in_place else _tensor(dst[i], "dst", dtype, (B, Dmax, w), dev)]
     if len(rows) == 1:
         arrays += [None, 0, None]
+    f32, i32 = torch.float32, torch.int32
+    sp, pp = _tensor(score, "score", f32, (B, Lmax), dev), _tensor(pos, "pos", i32, (B, Lmax), dev)
+    dsp = sp if in_place else _tensor(dst_score, "dst_score", f32, (B, Dmax), dev)
+    dpp = pp if in_place else _tensor(dst_pos, "dst_pos", i32, (B, Dmax), dev)
     wp, wb = _workspace(workspace, dev)
     code = lib.gmla_cache_evict(
-        *arrays, _tensor(score, "score", torch.float32, (B, Lmax), dev),
-        _tensor(dst_score, "dst_score", torch.float32, (B, Dmax), dev), _tensor(pos, "pos", torch.int32, (B, Lmax), dev),
-        _tensor(dst_pos, "dst_pos", torch.int32, (B, Dmax), dev), B, Lmax, Dmax, int(L),
-        _tensor(lens, "lens", torch.int32, (B,), dev), keep, int(sink), int(recent),
-        _tensor(new_lens, "new_lens", torch.int32, (B,), dev), _tensor(index, "index", torch.int32, (B, keep), dev),
-        wp, wb, _raw_stream(stream, dev))
+        *arrays, sp, dsp, pp, dpp, B, Lmax, Dmax, int(L), _tensor(lens, "lens", i32, (B,), dev), keep, int(sink),
+        int(recent), _tensor(new_lens, "new_lens", i32, (B,), dev), _tensor(index, "index", i32, (B, keep), dev), wp, wb,
+        _raw_stream(stream, dev))
     return _check(code, "gmla_cache_evict") if check else code
 
 
