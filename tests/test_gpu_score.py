@@ -93,6 +93,11 @@ def test_several_groups_of_sequences(g):
     run(g, 23, 65536, 65536, 96, 64, lens=[65536] + [1000 * k + 7 for k in range(21)] + [0])
 
 
+def test_several_groups_with_few_heads(g):
+    """The same where q~ has three parts (512 MB: 32 sequences of 65536 rows at 33 to 64 heads)."""
+    run(g, 34, 65536, 65536, 33, 64, lens=[70] * 31 + [65536, 0, 4001])
+
+
 def test_accumulates_over_captured_steps(g):
     rng = np.random.default_rng(4)
     B, L, H, d_c = 3, 600, 96, 512
