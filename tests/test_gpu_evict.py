@@ -122,6 +122,17 @@ def test_more_protected_than_kept(g):
     check(g, 1, 300, 300, 20, sink=5, recent=5, positions=pos)
 
 
+@pytest.mark.parametrize("L", [700, 9000])
+def test_positions_at_the_ends_of_their_type(g, L):
+    """Differences of 32-bit positions pass 32 bits."""
+    rng = np.random.default_rng(L)
+    ends = np.array([-2 ** 31, -2 ** 31 + 1, -1, 0, 5, 2 ** 31 - 2, 2 ** 31 - 1])
+    for top in (7, 5, 2, 1):  # with and without large positions: the recent ones reach below the lowest
+        pos = rng.choice(ends[:top], (2, L))
+        for sink, recent in ((0, 0), (0, 3), (5, 0), (2, 100)):
+            check(g, 2, L, L, 300, sink=sink, recent=recent, positions=pos, seed=top)
+
+
 def test_without_positions(g):
     check(g, 2, 700, 720, 300, sink=4, recent=32, with_pos=False)
 
