@@ -6,9 +6,10 @@
 //   S = hi C^T + lo C^T (+ third C^T)
 // on tcgen05 tensor cores, float32 accumulators; the rows c are bfloat16 as they are.  Two
 // kinds of errors matter: what two parts leave (17 bits), and the accumulators' rounding,
-// which grows with the MMAs that add to a sum of full size (64 a tile at d_c = 512).  Both
-// average out over heads: at 96 heads they are 7e-7 relative in all, at one head 4e-6.  So
-// up to 64 heads (FEW) q~ has a third part, and lo and third add up in an accumulator of their own.
+// which grows with the MMAs that add to a sum of full size (64 a tile at d_c = 512; its mean is
+// made up for, see sum_shortfall()).  Both average out over heads: at 96 heads they are 6e-7 relative
+// in all, at one head 3e-6.  So up to 64 heads (FEW) q~ has a third part, and lo and third
+// add up in an accumulator of their own: 2e-7 at 16 to 64 heads, 3e-7 at one.
 //
 // Two launches per group of sequences.
 //  scores_kernel   S of every (head, row), stored as float32, and per piece the running
@@ -478,6 +479,18 @@ __global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
 
 }  // namespace cache_score
 
+// By how much a score comes out nearer to zero, in 2^-24 of itself.  The tensor cores cut off what an addition leaves
+// below the accumulator's last bit, toward zero, so the shortfall grows with the MMAs of a sum, and as steps and scores grow
+// together it does not depend on size.  Fitted on B200 to log-weight errors against float64, regressed on the score
+// (random rows, d_c = 64 .. 512, 60 to 400 inputs each): within 1 of what was measured, from 5 to 26 above 64
+// heads, 2.3 to 9 below.  q~ is scaled up by it, which leaves only the errors' spread (96 heads, d_c = 512: 6.5e-7 to
+// 9.4e-7 without it, 5.1e-7 to 7.1e-7 with it; 64 heads 2.7e-7 and 1.7e-7).
+static double sum_shortfall(int H, int dc) {
+  const int chunks = dc / 64;
+  if (H > kScoreFewHeads) return 2. + 3. * chunks;  // hi and lo add to one sum by turns
+  return 1.5 + 0.9 * (H <= 32 && chunks > 1 ? chunks / 2. : chunks);
+}
+
 template <bool FEW>
 static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t stream) {
   using namespace cache_score;
@@ -486,9 +499,9 @@ static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t st
   const ScoreLayout lay = score_layout(reinterpret_cast<uintptr_t>(ws), a.B, a.L, a.H, a.dc);
   uint16_t *hi = reinterpret_cast<uint16_t *>(ws + lay.hi), *lo = reinterpret_cast<uint16_t *>(ws + lay.lo),
            *third = FEW ? reinterpret_cast<uint16_t *>(ws + lay.third) : nullptr;
-  constexpr float kLog2e = 1.4426950408889634f;
+  const float q_scale = (float)(a.scale * 1.4426950408889634 * (1. + sum_shortfall(a.H, a.dc) * 0x1p-24));
   if (!set_smem_limit_once(reinterpret_cast<const void *>(scores_kernel<FEW>), (int)smem, slot)) return -1;
-  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e, nullptr, hi, lo, third, a.status, stream) != 0)
+  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, q_scale, nullptr, hi, lo, third, a.status, stream) != 0)
     return -1;
   const int group = (int)score_group(a.B, a.L, a.H);
   for (int b0 = 0; b0 < a.B; b0 += group) {
