@@ -24,6 +24,16 @@ bool latent_width_ok(int64_t d_c) { return d_c % 64 == 0 && d_c <= 512; }
 // rows [r0, r0 + n) lie in 0..max - 1
 bool range_ok(int64_t r0, int64_t n, int64_t max) { return r0 >= 0 && n >= 1 && r0 <= max && n <= max - r0; }
 
+// An array's addresses [begin, end), in 128 bits: the sizes a call may name reach 2^72 bytes.
+struct Span {
+  unsigned __int128 begin, end;
+};
+Span span(const void *p, int64_t B, int64_t len_max, int64_t bytes) {
+  const unsigned __int128 begin = reinterpret_cast<uintptr_t>(p);
+  return {begin, begin + (unsigned __int128)B * (uint64_t)len_max * (uint64_t)bytes};
+}
+bool overlap(const Span &a, const Span &b) { return a.begin < b.end && b.begin < a.end; }
+
 }  // namespace
 
 extern "C" {
@@ -148,8 +158,7 @@ gmla_status gmla_cache_evict(const void *rows0, int64_t row_bytes0, void *dst0, 
   for (const auto &a : arrays) {
     if (!a.src) continue;
     if ((a.src == a.dst) != in_place) return GMLA_ERR_ARG;
-    const char *s = static_cast<const char *>(a.src), *d = static_cast<const char *>(a.dst);
-    if (!in_place && d < s + B * cache_len_max * a.bytes && s < d + B * dst_len_max * a.bytes) return GMLA_ERR_ARG;
+    if (!in_place && overlap(span(a.src, B, cache_len_max, a.bytes), span(a.dst, B, dst_len_max, a.bytes))) return GMLA_ERR_ARG;
   }
   if (in_place ? dst_len_max != cache_len_max : dst_len_max < (keep < L ? keep : L)) return GMLA_ERR_ARG;
   if (!workspace || workspace_bytes < gmla_cache_evict_workspace_size(B, L, keep)) return GMLA_ERR_WORKSPACE;
