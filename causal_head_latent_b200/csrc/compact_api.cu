@@ -161,7 +161,29 @@ gmla_status gmla_cache_evict(const void *rows0, int64_t row_bytes0, void *dst0, 
     if (!in_place && overlap(span(a.src, B, cache_len_max, a.bytes), span(a.dst, B, dst_len_max, a.bytes))) return GMLA_ERR_ARG;
   }
   if (in_place ? dst_len_max != cache_len_max : dst_len_max < (keep < L ? keep : L)) return GMLA_ERR_ARG;
-  if (!workspace || workspace_bytes < gmla_cache_evict_workspace_size(B, L, keep)) return GMLA_ERR_WORKSPACE;
+  const size_t need = gmla_cache_evict_workspace_size(B, L, keep);
+  if (!workspace || workspace_bytes < need) return GMLA_ERR_WORKSPACE;
+  // What the call writes lies apart from all else of it.  A source may be a destination's own (in place), the two row
+  // arrays may be one and the same, and new_lens may be lens.
+  Span in[5], out[7];
+  int n_in = 0, n_out = 0;
+  const bool twice = rows1 == rows0 && dst1 == dst0 && bytes[1] == bytes[0];
+  for (int i = 0; i < 4; ++i) {
+    const auto &a = arrays[i];
+    if (!a.src || (i == 1 && twice)) continue;
+    out[n_out++] = span(a.dst, B, dst_len_max, a.bytes);
+    if (!in_place) in[n_in++] = span(a.src, B, cache_len_max, a.bytes);
+  }
+  out[n_out++] = span(new_lens, B, 1, 4);
+  out[n_out++] = span(index, B, keep, 4);
+  out[n_out++] = span(workspace, 1, 1, need);
+  if (lens && lens != new_lens) in[n_in++] = span(lens, B, 1, 4);
+  for (int i = 0; i < n_out; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return GMLA_ERR_ARG;
+    for (int j = 0; j < n_in; ++j)
+      if (overlap(out[i], in[j])) return GMLA_ERR_ARG;
+  }
   if (!status_ptr()) return GMLA_ERR_CUDA;
   EvictArgs a{};
   a.rows[0] = EvictRows{rows0, dst0, (int)bytes[0], bytes[0] % 16 == 0};

@@ -556,6 +556,8 @@ GMLA_API size_t gmla_cache_score_workspace_size(int64_t B, int64_t L, int64_t H,
  *  index   int32 [B, keep] output: the row that row j came from, -1 for j >= n
  *  workspace >= gmla_cache_evict_workspace_size(B, L, keep) bytes, 16-byte
  *          aligned.  Calls that may overlap on the GPU need one each.
+ * What the call writes (destinations, new_lens, index, workspace) overlaps nothing else
+ * of it, but for a destination that is its source and new_lens that is lens.
  * Every pointer but scores', positions', lengths' and index's (4 bytes) is 16-byte aligned.
  * Errors: GMLA_ERR_ARG for null, misaligned or overlapping pointers and sizes
  * outside these bounds; GMLA_ERR_UNSUPPORTED for B > 65535 or lengths of 2^31 - 256 or
