@@ -7,8 +7,8 @@
 // accumulators:
 //   S      [head, key]  = q~ C_tile^T     M=128 (heads, padded by overlap), N=48 keys, K=d_c
 //   acc^T  [d_c, head] += C_tile^T P^T^T  M=128 per d_c block, N=96 heads, K=48 keys
-// Roundings: q~ to float16 (2^-12 relative, with scale * log2(e) * cache_scale folded
-// in) and P = 2^(S - m + 7) to float16.  The 7 keeps float16's range: the lazy maximum m
+// Roundings: q~ to float16 (2^-12 relative; scale * log2(e) * cache_scale and a power of two
+// per head are a float32 factor of S, see absorb_wide.cu) and P = 2^(S - m + 7) to float16.  The 7 keeps float16's range: the lazy maximum m
 // lets S - m reach 8, so P reaches 2^15, and a key is dropped only below 2^-32 of the
 // largest; without it, a million keys of weight 2^-25 each would vanish.  The row sum l
 // is float32 and takes the unrounded P; the factor 2^7 cancels in acc / l.
@@ -104,6 +104,7 @@ struct Params {
   long long Lmax;
   int H, dc;
   ShareBatch batch;
+  const float *q_factor;              // [B, H]: what S is multiplied with
   float *part_m, *part_l, *part_acc;  // [R, H], [R, H], [R, H, dc]; record = share + sequence
   unsigned *status;
 };
@@ -463,8 +464,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     uint8_t *prow = sp + (h >> 3) * P_SBO + (h & 7) * 16 + half * (HK / 8) * 128;
     bool ok = quarter < nq, gave_up = false;
+    grid_dependency_wait();  // the factors
     for (int i = 0, g = 0; ok && walk.next(batch, &pc); ++i) {
       float m_used = -INFINITY, l = 0.f;
+      const float f = head_ok ? p.q_factor[(size_t)pc.b * p.H + h] : 1.f;
       for (int j = 0; j < pc.n; ++j, ++g) {
         const int sb = g & 1;
         bool asked = false;
@@ -485,7 +488,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         float m4[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
         for (int c = 4; c < HK; ++c) m4[c & 3] = fmaxf(m4[c & 3], x[c]);
-        const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        const float mx = f * fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));  // f > 0 or NaN
         const bool need = head_ok && mx > m_used + kRescaleThreshold;
         if (bar_or(bar, 64, need || !ready)) {
           max_s[half * HMAX + h] = mx;
@@ -506,7 +509,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         uint32_t pk[HK / 2];
 #pragma unroll
         for (int c = 0; c < HK / 2; ++c) {
-          const float p0 = fast_exp2(x[2 * c] - mref), p1 = fast_exp2(x[2 * c + 1] - mref);
+          const float p0 = fast_exp2(fmaf(x[2 * c], f, -mref)), p1 = fast_exp2(fmaf(x[2 * c + 1], f, -mref));
           rs[c & 3] += p0 + p1;
           const __half2 v = __floats2half2_rn(p0, p1);
           pk[c] = *reinterpret_cast<const uint32_t *>(&v);
@@ -575,19 +578,19 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   const Fp4DecodeLayout lay = fp4_decode_layout(reinterpret_cast<uintptr_t>(ws), a.B, a.L, a.H, a.dc);
   uint16_t *qt = reinterpret_cast<uint16_t *>(ws + lay.qt);
-  float *pm = reinterpret_cast<float *>(ws + lay.pm), *pl = reinterpret_cast<float *>(ws + lay.pl);
+  float *qf = reinterpret_cast<float *>(ws + lay.qf), *pm = reinterpret_cast<float *>(ws + lay.pm), *pl = reinterpret_cast<float *>(ws + lay.pl);
   float *pacc = reinterpret_cast<float *>(ws + lay.pacc);
   const long long G = share_count(a.B, a.L, KT, kFp4PieceTiles);
   constexpr float kLog2e = 1.4426950408889634f;
   if (!set_smem_limit_once(reinterpret_cast<const void *>(decode_kernel), (int)smem_bytes(), kSmemLatentFp4)) return -1;
-  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e * a.cache_scale, qt, nullptr, nullptr, nullptr, a.status,
+  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, a.scale * kLog2e * a.cache_scale, qt, qf, nullptr, nullptr, nullptr, a.status,
                          stream) != 0)
     return -1;
   CUtensorMap tq;
   const long long dq[3] = {a.dc, a.H, a.B}, sq[2] = {a.dc, (long long)a.H * a.dc};
   const unsigned bq[3] = {64, HMAX, 1};
   if (!make_tmap_bf16(&tq, qt, 3, dq, sq, bq)) return -1;  // 2-byte elements, moved as they are
-  const Params p{a.codes, a.scales, a.cache_len_max, a.H, a.dc, ShareBatch{a.lens, a.B, a.L, KT, kFp4PieceTiles}, pm, pl, pacc, a.status};
+  const Params p{a.codes, a.scales, a.cache_len_max, a.H, a.dc, ShareBatch{a.lens, a.B, a.L, KT, kFp4PieceTiles}, qf, pm, pl, pacc, a.status};
   // Beginning beside the absorb kernel hides the set-up of a short launch (B=8 ragged to 16384:
   // 72 us against 76), and slows a long one (B=32, L=131072: 0.96 ms against 0.89).
   const long long tiles = (long long)a.B * ((a.L + KT - 1) / KT);

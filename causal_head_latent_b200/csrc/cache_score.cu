@@ -501,7 +501,7 @@ static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t st
            *third = FEW ? reinterpret_cast<uint16_t *>(ws + lay.third) : nullptr;
   const float q_scale = (float)(a.scale * 1.4426950408889634 * (1. + sum_shortfall(a.H, a.dc) * 0x1p-24));
   if (!set_smem_limit_once(reinterpret_cast<const void *>(scores_kernel<FEW>), (int)smem, slot)) return -1;
-  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, q_scale, nullptr, hi, lo, third, a.status, stream) != 0)
+  if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, q_scale, nullptr, nullptr, hi, lo, third, a.status, stream) != 0)
     return -1;
   const int group = (int)score_group(a.B, a.L, a.H);
   for (int b0 = 0; b0 < a.B; b0 += group) {

@@ -50,10 +50,10 @@ struct Fp4LoadArgs {
 int launch_fp4_load(const Fp4LoadArgs &a, cudaStream_t stream);
 
 // ---------------------------------------------------------------- absorbed queries
-// s * W_k^(h)T q_h for every (b, h): as float16 (f16 non-null, saturating) or as
+// s * W_k^(h)T q_h for every (b, h): as factor [B, H] times float16 (f16 non-null) or as
 // bfloat16 parts hi + lo (17 bits), and third unless null (24 bits); [B, H, dc].
 int launch_absorb_wide(const uint16_t *Q, const uint16_t *Wk, int B, int H, int dc, float s, uint16_t *f16,
-                       uint16_t *hi, uint16_t *lo, uint16_t *third, unsigned *status, cudaStream_t stream);
+                       float *factor, uint16_t *hi, uint16_t *lo, uint16_t *third, unsigned *status, cudaStream_t stream);
 
 // ---------------------------------------------------------------- decode over 4-bit rows
 struct Fp4DecodeArgs {

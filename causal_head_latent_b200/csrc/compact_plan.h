@@ -46,9 +46,9 @@ inline long long share_records(long long B, long long L, int tile, int extra) {
   return share_count(B, L, tile, extra) + B - 1;
 }
 
-// 4-bit decode: q~ float16 [B,H,dc] | m, l float [R,H] | acc float [R,H,dc].
+// 4-bit decode: q~ float16 [B,H,dc] | its factors float [B,H] | m, l float [R,H] | acc float [R,H,dc].
 struct Fp4DecodeLayout {
-  size_t qt, pm, pl, pacc, end;
+  size_t qt, qf, pm, pl, pacc, end;
 };
 inline Fp4DecodeLayout fp4_decode_layout(uintptr_t base, long long B, long long L, long long H, long long dc) {
   const size_t R = (size_t)share_records(B, L, kFp4TileKeys, kFp4PieceTiles);
@@ -56,6 +56,8 @@ inline Fp4DecodeLayout fp4_decode_layout(uintptr_t base, long long B, long long 
   size_t off = ws_round(base) - base;
   o.qt = off;
   off += ws_round(2 * (size_t)B * H * dc);
+  o.qf = off;
+  off += ws_round(4 * (size_t)B * H);
   o.pm = off;
   off += ws_round(4 * R * H);
   o.pl = off;

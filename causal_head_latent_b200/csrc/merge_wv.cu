@@ -154,6 +154,8 @@ __global__ void __launch_bounds__(THREADS, 1) merge_wv_kernel(const __grid_const
               }
         }
         l = warp_sum(l);
+        // every score -inf or NaN: NaN, not the zeros of an empty sequence
+        if (m == -INFINITY) l = __uint_as_float(0x7fffffffu);
       }
     }
     if (wps > 1) {  // nb <= WARPS / wps: one turn of the loop, every warp in it

@@ -52,6 +52,17 @@ __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The same in two steps, without release: for barriers made visible by fence_barrier_init().
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Store of a word to another CTA (cluster addresses from mapa_shared); the barrier there counts its 4 bytes.
+__device__ __forceinline__ void store_to_peer(uint32_t dst_cluster, uint32_t v, uint32_t bar_cluster) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(dst_cluster), "r"(v),
+               "r"(bar_cluster)
+               : "memory");
+}
+
 // Bulk copy from this CTA's shared memory to another CTA's (cluster addresses
 // from mapa_shared); completion is signalled on the destination's mbarrier.
 __device__ __forceinline__ void bulk_copy_to_peer(uint32_t dst_cluster, const void *src, uint32_t bytes,

@@ -487,7 +487,10 @@ GMLA_API gmla_status gmla_cache_dequantize_fp4(const uint8_t *codes, const uint8
  *          launch).  A sequence of length 0 gets O = 0.  Read when the kernels
  *          run, so a captured call follows the array's current values.
  *  Rows that are not visible are never read.
- *  Q, W_k, W_v, scale, G, O as gmla_attend_decode.
+ *  Q, W_k, W_v, scale, G, O as gmla_attend_decode.  The absorbed query is held in
+ *          float16 under a power of two of its own per sequence and head, so neither its
+ *          size nor cache_scale's is limited; one that is not finite makes its head's O NaN,
+ *          as do scores that are all past float32's range.
  *  workspace >= gmla_attend_decode_fp4_workspace_size(B, L, H, d_c) bytes, 16-byte
  *          aligned.  Calls that may overlap on the GPU need one each.
  * Errors as gmla_attend_decode; GMLA_ERR_ARG also for a bad cache_scale.
