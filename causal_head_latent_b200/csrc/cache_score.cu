@@ -344,6 +344,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
 // Each head's log-sum-exp from the states of a sequence's pieces, by `threads` threads of a
 // block, several per head; the records in a fixed order.  lse: shared or global memory.
+// A piece whose maximum is -infinity counts with its sum as it is: 0, or NaN where a score is
+// (maxima pass over NaN, sums do not), which then reaches every row of the sequence.
 struct JoinParams {
   ShareBatch batch;
   long long G;
@@ -372,8 +374,7 @@ __device__ __forceinline__ void join_pieces(const JoinParams &p, int b, long lon
       l *= m == -INFINITY ? 0.f : exp2f(m - mx);
       m = mx;
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (pm[k] != -INFINITY) l += pl[k] * exp2f(pm[k] - m);
+      for (int k = 0; k < 8; ++k) l += pm[k] != -INFINITY ? pl[k] * exp2f(pm[k] - m) : pl[k];
     }
   }
   m_s[threadIdx.x] = m;
@@ -383,8 +384,8 @@ __device__ __forceinline__ void join_pieces(const JoinParams &p, int b, long lon
     for (int k = 1; k < per; ++k) m = fmaxf(m, m_s[threadIdx.x + k * p.Hp]);
     float sum = 0.f;
     for (int k = 0; k < per; ++k) {
-      const float mk = m_s[threadIdx.x + k * p.Hp];
-      if (mk != -INFINITY) sum += l_s[threadIdx.x + k * p.Hp] * exp2f(mk - m);
+      const float mk = m_s[threadIdx.x + k * p.Hp], lk = l_s[threadIdx.x + k * p.Hp];
+      sum += mk != -INFINITY ? lk * exp2f(mk - m) : lk;
     }
     lse[threadIdx.x] = m + log2f(sum);
   }

@@ -515,6 +515,8 @@ GMLA_API size_t gmla_attend_decode_fp4_workspace_size(int64_t B, int64_t L, int6
  *  Q, C, W_k, scale  as gmla_attend_decode
  *  L, lens  as gmla_attend_decode_fp4 (lens: optional DEVICE int32 array).  Scores of
  *          rows at or past a sequence's length are left as they were.
+ *          Q and the visible rows should be finite: a NaN among a sequence's rows or in its
+ *          query makes all its scores NaN, and so does an infinity unless it only gives weights of 0.
  *  decay   finite; 1 accumulates, less than 1 forgets, 0 overwrites (score is then not read)
  *  score   float32 [B, cache_len_max], in/out
  *  workspace >= gmla_cache_score_workspace_size(B, L, H, d_c) bytes, 16-byte
