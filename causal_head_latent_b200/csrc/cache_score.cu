@@ -5,11 +5,16 @@
 // weights should not carry bfloat16's 8 bits: q~ goes in as parts, and
 //   S = hi C^T + lo C^T (+ third C^T)
 // on tcgen05 tensor cores, float32 accumulators; the rows c are bfloat16 as they are.  Two
-// kinds of errors matter: what two parts leave (17 bits), and the accumulators' rounding,
-// which grows with the MMAs that add to a sum of full size (64 a tile at d_c = 512; its mean is
-// made up for, see sum_shortfall()).  Both average out over heads: at 96 heads they are 6e-7 relative
-// in all, at one head 3e-6.  So up to 64 heads (FEW) q~ has a third part, and lo and third
-// add up in an accumulator of their own: 2e-7 at 16 to 64 heads, 3e-7 at one.
+// kinds of errors matter, and both average out over heads:
+//  * what two parts leave of q~ (2^-18 of an element at most);
+//  * the accumulators' rounding: an addition cuts off, toward zero, what lies below a sum's last
+//    bit, so the error grows with the MMAs that add to one sum of full size.  So a tile has two
+//    sums, of half the channels each (32 MMAs at d_c = 512), that are added in float32.
+// Up to 64 heads (FEW) q~ has a third part, and lo and third add up in an accumulator of their
+// own, so that one sum of hi takes as few.
+// Relative error of the weights, 30 inputs of 8 sequences to 5000 rows, median and largest: 96
+// heads, d_c = 512 5.4e-7 and 7.6e-7 (two parts alone leave 5e-7); 64 heads 2.3e-7 and 4.1e-7; one
+// 4.4e-7 and 7.5e-7.  Products in float32: 1.6-4.7e-7 and 8e-7.
 //
 // Two launches per group of sequences.
 //  scores_kernel   S of every (head, row), stored as float32, and per piece the running
@@ -30,12 +35,15 @@
 //   warp 1       TMEM owner; issues the MMAs (converged, one lane predicated)
 //   warp 2       TMA of q~ hi (and lo)
 //   warps 4..7   q~ lo (FEW: third) into TMEM; per tile the running softmax state and the store of S
+// A tile's first sum goes into registers while the second grows, and the second as soon as it is
+// there, before the work on them: the next tile's MMAs wait for neither.  (Both left in place until a
+// loop over the tile has read them: 48 us for 43 at B=8, ragged to 16384, 1.51 ms for 1.37 at B=32, L=131072.)
 // FEW: rows 0..63 of the A tile are hi and rows 64..127 lo, in shared memory (128 KB, so five
 // slots are left); third is in tensor memory, lanes 64..127, over zeros: as many MMAs as
 // above.  The warps of lanes 64..127 hand their sums to those of the heads through shared memory.
 // Up to 32 heads the second half of hi's chunks stands 32 rows lower, so that it adds up in
 // lanes 32..63, and those are handed over too (one head, d_c = 512: 1.4e-6 to 6e-7).
-// TMEM: D buffers at columns 0 and 128, q~ lo at 256 (a column holds two elements).
+// TMEM: sums at columns 0, 128 and, where there is room, 256; q~'s last part at the end (two elements a column).
 #include <math.h>
 
 #include "compact.h"
@@ -52,7 +60,7 @@ constexpr int KT = kScoreTileKeys;
 constexpr int NUM_THREADS = 256;
 constexpr int NCHUNK = 8;                   // 64-wide d_c chunks (d_c <= 512)
 constexpr int CCHUNK = KT * 128;            // 128 rows x 64 columns
-constexpr int TM_D = 0, TM_LO = 256;
+constexpr int ND = 3;                       // sums in tensor memory (2 where q~'s parts leave no more)
 constexpr unsigned long long kDrainLimitNs = 100000000ull;
 
 // Shared memory for up to kScoreFewHeads heads (FEW) and for more.
@@ -65,7 +73,7 @@ struct Plan {
   static constexpr int HAND_BYTES = FEW ? 2 * 2 * 32 * 128 : 0;  // two buffers of 32 sums per lane for two warps
   // !FEW: rows 96..127 of a 128-row A tile alias what follows: S rows nobody reads
   static_assert(QCHUNK >= 128 * 128 || NSLOT * CCHUNK >= 32 * 128, "the ring covers the q~ tail");
-  static constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + HAND_BYTES + 8 * (2 * NSLOT + 8) + 20; }
+  static constexpr size_t smem_bytes() { return Q_BYTES + NSLOT * CCHUNK + HAND_BYTES + 8 * (2 * NSLOT + 2 * ND + 4) + 20; }
 };
 static_assert(Plan<true>::smem_bytes() <= 232448 && Plan<false>::smem_bytes() <= 232448,
               "dynamic shared memory above the 227 KB a CTA may have");
@@ -81,6 +89,33 @@ struct Params {
   unsigned *status;
 };
 
+// The sums of a tile, one or two of `n` in tensor memory in turn, and the phases of their barriers.
+struct TileSums {
+  int at[2];
+  uint32_t phase[2];
+};
+struct SumRing {
+  int n;
+  bool two;
+  int at;
+  uint32_t phase;
+  __device__ __forceinline__ TileSums next() {
+    TileSums t;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      t.at[i] = at;
+      t.phase[i] = phase;
+      if (i == 1 || two) {
+        if (++at == n) {
+          at = 0;
+          phase ^= 1;
+        }
+      }
+    }
+    return t;
+  }
+};
+
 template <bool FEW>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     scores_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmT,
@@ -91,9 +126,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   float4 *hand = reinterpret_cast<float4 *>(sc + NSLOT * CCHUNK);      // [2][2][8][32]
   uint64_t *full = reinterpret_cast<uint64_t *>(sc + NSLOT * CCHUNK + Plan<FEW>::HAND_BYTES);  // [NSLOT]
   uint64_t *empty = full + NSLOT;                                      // [NSLOT]
-  uint64_t *d_full = empty + NSLOT;                                    // [2]
-  uint64_t *d_free = d_full + 2;                                       // [2]
-  uint64_t *q_full = d_free + 2, *q_free = q_full + 1, *lo_full = q_full + 2, *idle = q_full + 3;
+  uint64_t *d_full = empty + NSLOT;                                    // [ND]
+  uint64_t *d_free = d_full + ND;                                      // [ND]
+  uint64_t *q_full = d_free + ND, *q_free = q_full + 1, *lo_full = q_full + 2, *idle = q_full + 3;
   int *start = reinterpret_cast<int *>(idle + 1);  // [4]: where this share begins (ShareWalk), its tiles
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(start + 4);
 
@@ -106,7 +141,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ND; ++i) {
       mbar_init(&d_full[i], 1);
       mbar_init(&d_free[i], 4);
     }
@@ -142,6 +177,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   ShareWalk walk{start[0], start[1], start[2]};
   SharePiece pc{};
+  // the parts of q~ in tensor memory, at its end; the sums from its start
+  const int parts = nchunk, tm_lo = 512 - 32 * parts;
+  SumRing ring{parts <= 4 ? 3 : 2, !FEW && nchunk > 1, 0, 0};
 
   if (warp == 0) {
     if (lane == 0) {
@@ -172,35 +210,41 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t aq = smem_u32(sq), ac = smem_u32(sc);
     bool ok = true;
     int c = 0;
-    for (int i = 0, g = 0; ok && walk.next_uniform(batch, &pc); ++i) {
+    for (int i = 0; ok && walk.next_uniform(batch, &pc); ++i) {
       ok = warp_wait(q_full, i & 1, p.status);
-      for (int j = 0; ok && j < pc.n; ++j, ++g) {
-        if (g >= 2) ok = warp_wait_relaxed(&d_free[g & 1], ((g - 2) >> 1) & 1, p.status);
-        const uint32_t d = tmem + TM_D + (g & 1) * 128;
+      for (int j = 0; ok && j < pc.n; ++j) {
         // A piece's first tile takes the products of shared memory first, while the last part is on its way
         // to TMEM, if the ring holds the whole tile; the others take both per chunk.
         const int rounds = j == 0 && nchunk <= NSLOT ? 2 : 1;
+        const TileSums sums = ring.next();
         for (int r = 0; ok && r < rounds; ++r) {
           const bool do_hi = r == 0, do_lo = r == rounds - 1;
           if (j == 0 && do_lo) ok = warp_wait(lo_full, i & 1, p.status);
           for (int kc = 0; ok && kc < nchunk; ++kc) {
-            const int slot = (c + kc) % NSLOT;
-            if (do_hi) ok = warp_wait_relaxed(&full[slot], ((c + kc) / NSLOT) & 1, p.status);
+            const int slot = (c + kc) % NSLOT, half = FEW ? 0 : nchunk / 2;  // chunks of the first of two sums
+            const int sum = kc < half ? sums.at[0] : sums.at[1];
+            const bool begins = kc == 0 || kc == half;
+            if (do_hi && begins)
+              ok = warp_wait_relaxed(&d_free[sum], (kc < half ? sums.phase[0] : sums.phase[1]) ^ 1, p.status);
+            if (ok && do_hi) ok = warp_wait_relaxed(&full[slot], ((c + kc) / NSLOT) & 1, p.status);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t a = aq + kc * QCHUNK, b = ac + slot * CCHUNK, alo = tmem + TM_LO + kc * 32;
+            const uint32_t a = aq + kc * QCHUNK, b = ac + slot * CCHUNK, alo = tmem + tm_lo + kc * 32, d = tmem + sum * 128;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
               const uint64_t db = sdesc_sw128(b + kk * 32, 16, 1024);
-              if (do_hi) umma_f16_ss_if(issue, d, sdesc_sw128(a + kk * 32, 16, 1024), db, id, (kc | kk) ? 1u : 0u);
+              if (do_hi) umma_f16_ss_if(issue, d, sdesc_sw128(a + kk * 32, 16, 1024), db, id, begins && kk == 0 ? 0u : 1u);
               if (do_lo) umma_f16_ts_if(issue, d, alo + kk * 8, db, id, 1u);
             }
-            if (do_lo) umma_commit_if(issue, &empty[slot]);
+            if (do_lo) {
+              umma_commit_if(issue, &empty[slot]);
+              if (kc == half - 1) umma_commit_if(issue, &d_full[sums.at[0]]);
+            }
           }
         }
         c += nchunk;
         if (!ok) break;
-        umma_commit_if(issue, &d_full[g & 1]);
+        umma_commit_if(issue, &d_full[sums.at[1]]);
       }
       if (ok) umma_commit_if(issue, q_free);
     }
@@ -236,7 +280,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const bool gives = halves ? quarter > 0 : quarter >= 2;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     bool ok = true;
-    for (int i = 0, g = 0; ok && walk.next(batch, &pc); ++i) {
+    for (int i = 0; ok && walk.next(batch, &pc); ++i) {
       if (i == 0) grid_dependency_wait();
       // The last part of q~ of the piece (the MMAs of the piece before are done: its last d_full was waited for).
       const int hq = FEW ? h - 64 : h;
@@ -244,12 +288,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint4 *src = reinterpret_cast<const uint4 *>(p.last + ((size_t)pc.b * p.H + (q_ok ? hq : 0)) * p.dc);
 #pragma unroll 1
       for (int k0 = 0; k0 < nchunk; k0 += 4) {  // four chunks' loads in flight
+        const int n = min(4, nchunk - k0), at = tm_lo + k0 * 32;
         uint4 w[4][8];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            w[c][k] = q_ok && k0 + c < nchunk ? src[(k0 + c) * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
+          for (int k = 0; k < 8; ++k) w[c][k] = q_ok && c < n ? src[(k0 + c) * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v[32];
@@ -260,46 +304,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             v[4 * k + 2] = __uint_as_float(w[c][k].z);
             v[4 * k + 3] = __uint_as_float(w[c][k].w);
           }
-          if (k0 + c < nchunk) tmem_st32(tmem + lane_off + TM_LO + (k0 + c) * 32, v);
+          if (c < n) tmem_st32(tmem + lane_off + at + c * 32, v);
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(lo_full);
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < pc.n; ++j, ++g) {
-        ok = warp_wait(&d_full[g & 1], (g >> 1) & 1, p.status);
+      for (int j = 0; j < pc.n; ++j) {
+        const TileSums sums = ring.next();
+        float y[KT / 32][32];  // !FEW: the tile
+        if (!FEW) {  // the first of two sums is taken while the second grows, and both before the work on them
+          if (ring.two) ok = warp_wait(&d_full[sums.at[0]], sums.phase[0], p.status);
+          tc_fence_after();
+#pragma unroll
+          for (int k = 0; k < KT / 32; ++k) tmem_ld32(tmem + lane_off + sums.at[0] * 128 + 32 * k, y[k]);
+          tc_fence_before();
+          __syncwarp();
+          if (ring.two && ok && lane == 0) mbar_arrive(&d_free[sums.at[0]]);
+        }
+        ok = ok && warp_wait(&d_full[sums.at[1]], sums.phase[1], p.status);
         if (FEW && in_use) ok = !bar_or(bar, bar_threads, !ok);  // all warps of a head go on or all leave
         if (!ok) break;
         tc_fence_after();
+        if (!FEW) {
+#pragma unroll
+          for (int k = 0; k < KT / 32; ++k) {
+            float x[32];
+            tmem_ld32(tmem + lane_off + sums.at[1] * 128 + 32 * k, x);
+#pragma unroll
+            for (int n = 0; n < 32; ++n) y[k][n] = ring.two ? x[n] + y[k][n] : x[n];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&d_free[sums.at[1]]);
+        }
         const int left = pc.len - (pc.tile0 + j) * KT;  // visible rows of this tile
         float4 *out = reinterpret_cast<float4 *>(p.S) +
                       (((size_t)pc.b * p.tiles_max + pc.tile0 + j) * (KT / 4)) * p.Hp + h;
-#pragma unroll 1
-        for (int c0 = 0; c0 < KT; c0 += 32) {
-          float x[32];
-          if (in_use) tmem_ld32(tmem + lane_off + TM_D + (g & 1) * 128 + c0, x);
-          if (c0 + 32 == KT) {  // the last read of this D buffer
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&d_free[g & 1]);
-          }
-          if (FEW && in_use) {  // two buffers by turns: the one before last was read before this barrier's last turn
-            float4 *buf = hand + ((c0 / 32 & 1) * 2 + (quarter & 1)) * 256 + lane;
-            if (gives)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) buf[32 * k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-            bar_sync(bar, bar_threads);
-            for (int from = 0; !gives && from < (halves ? 2 : 1); ++from)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 v = buf[256 * from + 32 * k];
-                x[4 * k] += v.x;
-                x[4 * k + 1] += v.y;
-                x[4 * k + 2] += v.z;
-                x[4 * k + 3] += v.w;
-              }
-          }
+        // 32 rows from c0 of the tile: S out, and into the running state
+        auto take = [&](int c0, float (&x)[32]) {
           if (head_ok && left > c0) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -323,6 +367,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             l += (rs[0] + rs[1]) + (rs[2] + rs[3]);
           }
           __syncwarp();
+        };
+        if (!FEW) {
+#pragma unroll
+          for (int k = 0; k < KT / 32; ++k) take(32 * k, y[k]);
+        } else {
+#pragma unroll 1
+          for (int c0 = 0; c0 < KT; c0 += 32) {
+            float x[32];
+            if (in_use) tmem_ld32(tmem + lane_off + sums.at[1] * 128 + c0, x);
+            if (c0 + 32 == KT) {  // the last read of this sum
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&d_free[sums.at[1]]);
+            }
+            if (in_use) {  // two buffers by turns: the one before last was read before this barrier's last turn
+              float4 *buf = hand + ((c0 / 32 & 1) * 2 + (quarter & 1)) * 256 + lane;
+              if (gives)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) buf[32 * k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+              bar_sync(bar, bar_threads);
+              for (int from = 0; !gives && from < (halves ? 2 : 1); ++from)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const float4 v = buf[256 * from + 32 * k];
+                  x[4 * k] += v.x;
+                  x[4 * k + 1] += v.y;
+                  x[4 * k + 2] += v.z;
+                  x[4 * k + 3] += v.w;
+                }
+            }
+            take(c0, x);
+          }
         }
       }
       if (ok && head_ok) {
@@ -480,18 +556,6 @@ __global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
 
 }  // namespace cache_score
 
-// By how much a score comes out nearer to zero, in 2^-24 of itself.  The tensor cores cut off what an addition leaves
-// below the accumulator's last bit, toward zero, so the shortfall grows with the MMAs of a sum, and as steps and scores grow
-// together it does not depend on size.  Fitted on B200 to log-weight errors against float64, regressed on the score
-// (random rows, d_c = 64 .. 512, 60 to 400 inputs each): within 1 of what was measured, from 5 to 26 above 64
-// heads, 2.3 to 9 below.  q~ is scaled up by it, which leaves only the errors' spread (96 heads, d_c = 512: 6.5e-7 to
-// 9.4e-7 without it, 5.1e-7 to 7.1e-7 with it; 64 heads 2.7e-7 and 1.7e-7).
-static double sum_shortfall(int H, int dc) {
-  const int chunks = dc / 64;
-  if (H > kScoreFewHeads) return 2. + 3. * chunks;  // hi and lo add to one sum by turns
-  return 1.5 + 0.9 * (H <= 32 && chunks > 1 ? chunks / 2. : chunks);
-}
-
 template <bool FEW>
 static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t stream) {
   using namespace cache_score;
@@ -500,7 +564,7 @@ static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t st
   const ScoreLayout lay = score_layout(reinterpret_cast<uintptr_t>(ws), a.B, a.L, a.H, a.dc);
   uint16_t *hi = reinterpret_cast<uint16_t *>(ws + lay.hi), *lo = reinterpret_cast<uint16_t *>(ws + lay.lo),
            *third = FEW ? reinterpret_cast<uint16_t *>(ws + lay.third) : nullptr;
-  const float q_scale = (float)(a.scale * 1.4426950408889634 * (1. + sum_shortfall(a.H, a.dc) * 0x1p-24));
+  const float q_scale = (float)(a.scale * 1.4426950408889634 );
   if (!set_smem_limit_once(reinterpret_cast<const void *>(scores_kernel<FEW>), (int)smem, slot)) return -1;
   if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, q_scale, nullptr, nullptr, hi, lo, third, a.status, stream) != 0)
     return -1;

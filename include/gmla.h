@@ -509,8 +509,10 @@ GMLA_API size_t gmla_attend_decode_fp4_workspace_size(int64_t B, int64_t L, int6
  *     score[b, s] = decay * score[b, s] + sum_h a_bhs
  * with a_bhs the softmax weights of gmla_attend_decode (rows of every head sum
  * to 1, so a call adds H to the scores of a sequence).  What gmla_cache_evict
- * goes by.  Float32 throughout: the absorbed query is carried with 17 bits (two
- * bfloat16 parts), up to 64 heads with 24 (three), the cache rows as they are.
+ * goes by.  Scores, softmax statistics and weights are float32, the cache rows as they
+ * are.  The absorbed query q~ is carried with 24 bits (three bfloat16 parts) up to 64
+ * heads, beyond with 17 (two), where q~'s rounding moves a score by up to
+ * 2^-18 sum_c |q~_c C_sc| (weights of 96 heads at d_c = 512: 5e-7 relative, 2e-7 in float32).
  *
  *  Q, C, W_k, scale  as gmla_attend_decode
  *  L, lens  as gmla_attend_decode_fp4 (lens: optional DEVICE int32 array).  Scores of

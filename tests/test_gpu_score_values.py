@@ -61,3 +61,80 @@ def test_a_query_that_is_not_finite(g, value, H):
     got = score(g, Q, C, L, W_k, H)
     assert np.isnan(got[0]).all()
     assert np.linalg.norm(got[1] - want[1]) <= REL * np.linalg.norm(want[1])
+
+
+# ---- Sums that are exact, or nearly: queries that the parts of q~ hold exactly, the same in every head, so that no
+# error averages out.  A score scale of ln 2 makes scores base 2: the factor on q~ is exactly 1.
+LN2 = float(np.float32(np.log(2.0)))
+
+# Relative error of a row's weight where its score S is exact: float32 rounds S - lse (below 32 in size: 2^-20 at most) and
+# lse (below 16: 2^-21), log2f is off by a step (below 8: 2^-21), times ln 2; ex2 twice 2^-22; float32 sums of the heads
+# (8 roundings deep) and of the rows (24) 2^-24 each: 1.4e-6 + 5e-7 + 1.9e-6.
+EXACT = 4e-6
+
+
+def same_heads(H, d_c, w, q=(1.0,)):
+    """Q [1, H*128] and W_k [H*128, d_c] with q~ = sum_i q[i] w[i] in every head."""
+    Q, W = torch.zeros(1, H, 128), torch.zeros(H, 128, d_c)
+    for i, x in enumerate(q):
+        Q[:, :, i], W[:, i] = x, torch.from_numpy(w[i].astype(np.float32))
+    return Q.view(1, -1).to(torch.bfloat16).cuda(), W.view(H * 128, d_c).to(torch.bfloat16).cuda()
+
+
+def bf16(x):
+    return torch.from_numpy(np.asarray(x, np.float32)).to(torch.bfloat16).float().numpy().astype(np.float64)
+
+
+def weights_of(g, Q, rows, W_k, H):
+    C = torch.from_numpy(rows.astype(np.float32)).to(torch.bfloat16).cuda()[None]
+    got = score(g, Q, C, C.shape[1], W_k, H, scale=LN2)[0]
+    return got, plain(f64(Q), f64(C), [C.shape[1]], f64(W_k), H, LN2)[0]
+
+
+@pytest.mark.parametrize("H,d_c", [(96, 512), (65, 320), (96, 64), (64, 512), (33, 448), (7, 128), (1, 512)])
+def test_scores_of_one_channel_are_exact(g, H, d_c):
+    """One non-zero channel a row, scores from -10 to 10: nothing is rounded in a sum of one product, so the weights are
+    exact to float32 however large the score."""
+    rng = np.random.default_rng(d_c)
+    L = 700
+    w = bf16(rng.uniform(0.5, 2, d_c) * rng.choice([-1, 1], d_c))
+    Q, W_k = same_heads(H, d_c, [w])
+    rows, at = np.zeros((L, d_c)), rng.integers(0, d_c, L)
+    rows[np.arange(L), at] = bf16(rng.uniform(-10, 10, L) / w[at])
+    got, want = weights_of(g, Q, rows, W_k, H)
+    assert (np.abs(got - want) <= EXACT * want).all()
+
+
+@pytest.mark.parametrize("pattern", ["loud last", "loud first", "cancelling", "second half zero", "even"])
+@pytest.mark.parametrize("H,d_c", [(96, 512), (96, 256), (65, 64), (64, 512), (32, 384), (1, 512)])
+def test_sums_grow_in_any_order(g, H, d_c, pattern):
+    """Bound: each of the d_c / 16 additions to a sum cuts off less than a step of it, at most 2^-23 of the largest partial
+    sum or product, and as much again where 16 products meet; a row's weight moves by ln 2 times its score's error and
+    the log-sum-exp's, which is no more than the largest."""
+    rng = np.random.default_rng(d_c + H)
+    L = 900
+    w = bf16(rng.uniform(0.5, 2, d_c))
+    Q, W_k = same_heads(H, d_c, [w])
+    rows = rng.standard_normal((L, d_c))
+    size = np.ones(d_c)
+    if pattern == "loud last":
+        size[:-8] = 1 / 64
+    if pattern == "loud first":
+        size[8:] = 1 / 64
+    if pattern == "second half zero":
+        size[d_c // 2:] = 0
+    rows = rows * size
+    if pattern == "cancelling":  # what the first half adds up to, the second takes away, but for a few units
+        rows = np.abs(rows) * np.where(np.arange(d_c) < d_c // 2, 1, -1)
+    target = rng.uniform(-6, 6, L)
+    rows[:, -1] += (target - rows @ w) / w[-1] if pattern == "cancelling" else 0
+    if pattern != "cancelling":
+        rows *= (target / (rows @ w))[:, None].clip(-4, 4)
+    rows = bf16(rows)
+    keep = np.abs(rows @ w) < 10
+    rows = rows[keep]
+    got, want = weights_of(g, Q, rows, W_k, H)
+    products = rows * w
+    largest = max(np.abs(np.cumsum(products, 1)).max(), np.abs(np.cumsum(products[:, d_c // 2:], 1)).max(), np.abs(products).max())
+    off = d_c / 16 * 2 * 2.0 ** -23 * largest
+    assert (np.abs(got - want) <= (EXACT + 2 * np.log(2) * off) * want).all()
