@@ -11,10 +11,11 @@
 //    bit, so the error grows with the MMAs that add to one sum of full size.  So a tile has two
 //    sums, of half the channels each (32 MMAs at d_c = 512), that are added in float32.
 // Up to 64 heads (FEW) q~ has a third part, and lo and third add up in an accumulator of their
-// own, so that one sum of hi takes as few.
+// own, so that one sum of hi takes as few.  Above, a third part fits beside the sums up to
+// d_c = 256 (THIRD); at d_c = 512 it would take 96 of the ring's 128 KB.
 // Relative error of the weights, 30 inputs of 8 sequences to 5000 rows, median and largest: 96
-// heads, d_c = 512 5.4e-7 and 7.6e-7 (two parts alone leave 5e-7); 64 heads 2.3e-7 and 4.1e-7; one
-// 4.4e-7 and 7.5e-7.  Products in float32: 1.6-4.7e-7 and 8e-7.
+// heads, d_c = 512 5.4e-7 and 7.6e-7 (two parts alone leave 5e-7), d_c = 64 to 256 1.6-2.4e-7 and
+// 4.7e-7; 64 heads 2.3e-7 and 4.1e-7; one 4.4e-7 and 7.5e-7.  Products in float32: 0.7-4.7e-7 and 8e-7.
 //
 // Two launches per group of sequences.
 //  scores_kernel   S of every (head, row), stored as float32, and per piece the running
@@ -34,7 +35,7 @@
 //   warp 0       TMA of the rows, 64-column chunks
 //   warp 1       TMEM owner; issues the MMAs (converged, one lane predicated)
 //   warp 2       TMA of q~ hi (and lo)
-//   warps 4..7   q~ lo (FEW: third) into TMEM; per tile the running softmax state and the store of S
+//   warps 4..7   q~ lo (FEW: third; THIRD: both) into TMEM; per tile the running softmax state and the store of S
 // A tile's first sum goes into registers while the second grows, and the second as soon as it is
 // there, before the work on them: the next tile's MMAs wait for neither.  (Both left in place until a
 // loop over the tile has read them: 48 us for 43 at B=8, ragged to 16384, 1.51 ms for 1.37 at B=32, L=131072.)
@@ -43,7 +44,7 @@
 // above.  The warps of lanes 64..127 hand their sums to those of the heads through shared memory.
 // Up to 32 heads the second half of hi's chunks stands 32 rows lower, so that it adds up in
 // lanes 32..63, and those are handed over too (one head, d_c = 512: 1.4e-6 to 6e-7).
-// TMEM: sums at columns 0, 128 and, where there is room, 256; q~'s last part at the end (two elements a column).
+// TMEM: sums at columns 0, 128 and, where there is room, 256; q~'s last parts at the end (two elements a column).
 #include <math.h>
 
 #include "compact.h"
@@ -84,6 +85,7 @@ struct Params {
   long long tiles_max;      // tiles of a sequence in S
   ShareBatch batch;
   const uint16_t *last;     // the part in tensor memory (lo; FEW: third) [B, H, dc]
+  const uint16_t *behind;   // THIRD: third, behind lo there
   float *part_m, *part_l;   // [R, H]
   float *S;                 // [B][tiles_max][KT / 4][Hp][4]
   unsigned *status;
@@ -116,7 +118,7 @@ struct SumRing {
   }
 };
 
-template <bool FEW>
+template <bool FEW, bool THIRD>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     scores_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmT,
                   const __grid_constant__ CUtensorMap tmC, const Params p) {
@@ -178,7 +180,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   ShareWalk walk{start[0], start[1], start[2]};
   SharePiece pc{};
   // the parts of q~ in tensor memory, at its end; the sums from its start
-  const int parts = nchunk, tm_lo = 512 - 32 * parts;
+  const int parts = nchunk * (THIRD ? 2 : 1), tm_lo = 512 - 32 * parts;
   SumRing ring{parts <= 4 ? 3 : 2, !FEW && nchunk > 1, 0, 0};
 
   if (warp == 0) {
@@ -235,6 +237,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const uint64_t db = sdesc_sw128(b + kk * 32, 16, 1024);
               if (do_hi) umma_f16_ss_if(issue, d, sdesc_sw128(a + kk * 32, 16, 1024), db, id, begins && kk == 0 ? 0u : 1u);
               if (do_lo) umma_f16_ts_if(issue, d, alo + kk * 8, db, id, 1u);
+              if (THIRD && do_lo) umma_f16_ts_if(issue, d, alo + nchunk * 32 + kk * 8, db, id, 1u);
             }
             if (do_lo) {
               umma_commit_if(issue, &empty[slot]);
@@ -282,18 +285,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     bool ok = true;
     for (int i = 0; ok && walk.next(batch, &pc); ++i) {
       if (i == 0) grid_dependency_wait();
-      // The last part of q~ of the piece (the MMAs of the piece before are done: its last d_full was waited for).
+      // The last part of q~ of the piece (the MMAs of the piece before are done: its last d_full was waited for), or
+      // the last two of at most four chunks each.
       const int hq = FEW ? h - 64 : h;
       const bool q_ok = hq >= 0 && hq < p.H;
-      const uint4 *src = reinterpret_cast<const uint4 *>(p.last + ((size_t)pc.b * p.H + (q_ok ? hq : 0)) * p.dc);
+      const size_t row = ((size_t)pc.b * p.H + (q_ok ? hq : 0)) * p.dc;
+      const int n_tm = THIRD ? 4 + nchunk : nchunk;
 #pragma unroll 1
-      for (int k0 = 0; k0 < nchunk; k0 += 4) {  // four chunks' loads in flight
-        const int n = min(4, nchunk - k0), at = tm_lo + k0 * 32;
+      for (int k0 = 0; k0 < n_tm; k0 += 4) {  // four chunks' loads in flight
+        const bool second = THIRD && k0 > 0;
+        const uint4 *src = reinterpret_cast<const uint4 *>((second ? p.behind : p.last) + row) + (second ? 0 : k0 * 8);
+        const int n = min(4, second ? nchunk : nchunk - k0), at = tm_lo + (second ? nchunk : k0) * 32;
         uint4 w[4][8];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) w[c][k] = q_ok && c < n ? src[(k0 + c) * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
+          for (int k = 0; k < 8; ++k) w[c][k] = q_ok && c < n ? src[c * 8 + k] : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           float v[32];
@@ -556,16 +563,16 @@ __global__ void __launch_bounds__(ST) sum_kernel(const SumParams p) {
 
 }  // namespace cache_score
 
-template <bool FEW>
+template <bool FEW, bool THIRD>
 static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t stream) {
   using namespace cache_score;
   constexpr size_t smem = Plan<FEW>::smem_bytes();
   uint8_t *ws = static_cast<uint8_t *>(a.workspace);
   const ScoreLayout lay = score_layout(reinterpret_cast<uintptr_t>(ws), a.B, a.L, a.H, a.dc);
   uint16_t *hi = reinterpret_cast<uint16_t *>(ws + lay.hi), *lo = reinterpret_cast<uint16_t *>(ws + lay.lo),
-           *third = FEW ? reinterpret_cast<uint16_t *>(ws + lay.third) : nullptr;
+           *third = FEW || THIRD ? reinterpret_cast<uint16_t *>(ws + lay.third) : nullptr;
   const float q_scale = (float)(a.scale * 1.4426950408889634 );
-  if (!set_smem_limit_once(reinterpret_cast<const void *>(scores_kernel<FEW>), (int)smem, slot)) return -1;
+  if (!set_smem_limit_once(reinterpret_cast<const void *>(scores_kernel<FEW, THIRD>), (int)smem, slot)) return -1;
   if (launch_absorb_wide(a.Q, a.Wk, a.B, a.H, a.dc, q_scale, nullptr, nullptr, hi, lo, third, a.status, stream) != 0)
     return -1;
   const int group = (int)score_group(a.B, a.L, a.H);
@@ -587,6 +594,7 @@ static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t st
     p.tiles_max = score_tiles(a.L);
     p.batch = ShareBatch{a.lens ? a.lens + b0 : nullptr, nb, a.L, KT, kScorePieceTiles};
     p.last = (FEW ? third : lo) + (size_t)b0 * a.H * a.dc;
+    p.behind = THIRD ? third + (size_t)b0 * a.H * a.dc : nullptr;
     p.part_m = reinterpret_cast<float *>(ws + lay.pm);
     p.part_l = reinterpret_cast<float *>(ws + lay.pl);
     p.S = reinterpret_cast<float *>(ws + lay.s);
@@ -595,7 +603,7 @@ static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t st
     // Beginning beside a short launch hides 2 us (the sums at B=1, L=1001: 24.6 against 26.7); beside a
     // long one it takes from its bandwidth (B=32, L=131072: 1.49 ms against 1.39).
     const bool beside = p.tiles_max * nb <= 8 * kShares;
-    if (launch_beside(beside && b0 == 0, scores_kernel<FEW>, dim3((unsigned)G), dim3(NUM_THREADS), smem, stream, tq, tt, tc,
+    if (launch_beside(beside && b0 == 0, scores_kernel<FEW, THIRD>, dim3((unsigned)G), dim3(NUM_THREADS), smem, stream, tq, tt, tc,
                       p) != 0)
       return -1;
     SumParams u;
@@ -625,8 +633,9 @@ static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t st
 }
 
 int launch_cache_score(const ScoreArgs &a, cudaStream_t stream) {
-  return a.H <= kScoreFewHeads ? launch_cache_score<true>(a, kSmemScoreFew, stream)
-                               : launch_cache_score<false>(a, kSmemScore, stream);
+  if (a.H <= kScoreFewHeads) return launch_cache_score<true, false>(a, kSmemScoreFew, stream);
+  return score_has_third(a.H, a.dc) ? launch_cache_score<false, true>(a, kSmemScoreThird, stream)
+                                    : launch_cache_score<false, false>(a, kSmemScore, stream);
 }
 
 }  // namespace gmla

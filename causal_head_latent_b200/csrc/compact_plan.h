@@ -86,8 +86,9 @@ inline long long score_group(long long B, long long L, long long H) {
   return n < 1 ? 1 : n > B ? B : n;
 }
 
-// Up to this many heads q~ has a third part.
-constexpr int kScoreFewHeads = 64;
+// Up to this many heads, or this latent width, q~ has a third part.
+constexpr int kScoreFewHeads = 64, kScoreThirdWidth = 256;
+inline bool score_has_third(long long H, long long dc) { return H <= kScoreFewHeads || dc <= kScoreThirdWidth; }
 
 // q~ as bfloat16 hi, lo (and third) [B,H,dc] | of a group: m, l float [R,H], log-sum-exp float [n,H], scores.
 struct ScoreLayout {
@@ -103,7 +104,7 @@ inline ScoreLayout score_layout(uintptr_t base, long long B, long long L, long l
   o.lo = off;
   off += ws_round(2 * (size_t)B * H * dc);
   o.third = off;
-  if (H <= kScoreFewHeads) off += ws_round(2 * (size_t)B * H * dc);
+  if (score_has_third(H, dc)) off += ws_round(2 * (size_t)B * H * dc);
   o.pm = off;
   off += ws_round(4 * R * H);
   o.pl = off;

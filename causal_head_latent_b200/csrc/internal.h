@@ -118,7 +118,7 @@ int num_sms();
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current
 // device, once per (kernel slot, device): the attribute belongs to the
 // device's context, so a process that drives several GPUs sets it on each.
-enum SmemSlot { kSmemPrefill = 0, kSmemGemm = 1, kSmemLatentTc = 2, kSmemWv = 3, kSmemGemmSK = 4, kSmemRows = 5, kSmemAbsorbTc = 6, kSmemGemmSK192 = 7, kSmemLatentFp4 = 8, kSmemScore = 9, kSmemEvict1 = 10, kSmemEvict8 = 11, kSmemMergeWv = 12, kSmemScoreFew = 13, kSmemSlots = 14 };
+enum SmemSlot { kSmemPrefill = 0, kSmemGemm = 1, kSmemLatentTc = 2, kSmemWv = 3, kSmemGemmSK = 4, kSmemRows = 5, kSmemAbsorbTc = 6, kSmemGemmSK192 = 7, kSmemLatentFp4 = 8, kSmemScore = 9, kSmemEvict1 = 10, kSmemEvict8 = 11, kSmemMergeWv = 12, kSmemScoreFew = 13, kSmemScoreThird = 14, kSmemSlots = 15 };
 bool set_smem_limit_once(const void *kernel, int bytes, SmemSlot slot);
 
 // bf16 TMA tensor map with 128-byte swizzle; dims/strides in elements, dim 0 contiguous.

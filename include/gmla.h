@@ -511,7 +511,7 @@ GMLA_API size_t gmla_attend_decode_fp4_workspace_size(int64_t B, int64_t L, int6
  * to 1, so a call adds H to the scores of a sequence).  What gmla_cache_evict
  * goes by.  Scores, softmax statistics and weights are float32, the cache rows as they
  * are.  The absorbed query q~ is carried with 24 bits (three bfloat16 parts) up to 64
- * heads, beyond with 17 (two), where q~'s rounding moves a score by up to
+ * heads or d_c = 256; beyond both with 17 (two), where q~'s rounding moves a score by up to
  * 2^-18 sum_c |q~_c C_sc| (weights of 96 heads at d_c = 512: 5e-7 relative, 2e-7 in float32).
  *
  *  Q, C, W_k, scale  as gmla_attend_decode

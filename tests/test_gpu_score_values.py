@@ -138,3 +138,19 @@ def test_sums_grow_in_any_order(g, H, d_c, pattern):
     largest = max(np.abs(np.cumsum(products, 1)).max(), np.abs(np.cumsum(products[:, d_c // 2:], 1)).max(), np.abs(products).max())
     off = d_c / 16 * 2 * 2.0 ** -23 * largest
     assert (np.abs(got - want) <= (EXACT + 2 * np.log(2) * off) * want).all()
+
+
+@pytest.mark.parametrize("H,d_c", [(1, 512), (16, 512), (32, 64), (33, 448), (64, 512), (65, 256), (96, 256), (96, 192), (96, 64)])
+def test_a_query_of_24_bits_is_whole(g, H, d_c):
+    """q~ = 1 + a 2^-10 + b 2^-19, a and b in [1, 2), and rows that take the difference of two channels with the same a: the
+    scores are 4 (b - b'), all from the third part.  Sums are exact (a product cancels its pair's within one MMA)."""
+    rng = np.random.default_rng(d_c + H)
+    L = 800
+    a = np.repeat(1 + rng.integers(0, 128, d_c // 2) / 128, 2)
+    b = 1 + rng.integers(0, 8, d_c) / 8
+    Q, W_k = same_heads(H, d_c, [np.ones(d_c), a, b], (1.0, 2.0 ** -10, 2.0 ** -19))
+    rows, at = np.zeros((L, d_c)), 2 * rng.integers(0, d_c // 2, L)
+    rows[np.arange(L), at], rows[np.arange(L), at + 1] = 2.0 ** 21, -2.0 ** 21
+    got, want = weights_of(g, Q, rows, W_k, H)
+    assert want.max() > 3 * want.min()
+    assert (np.abs(got - want) <= EXACT * want).all()
