@@ -154,3 +154,17 @@ def test_a_query_of_24_bits_is_whole(g, H, d_c):
     got, want = weights_of(g, Q, rows, W_k, H)
     assert want.max() > 3 * want.min()
     assert (np.abs(got - want) <= EXACT * want).all()
+
+
+@pytest.mark.parametrize("H,d_c", [(1, 512), (64, 512), (65, 448), (96, 512), (96, 320), (96, 256), (96, 64)])
+def test_a_query_of_17_bits_is_whole(g, H, d_c):
+    """The same with q~ = 1 + a 2^-10 and scores 4 (a - a'), all from the second part."""
+    rng = np.random.default_rng(d_c + H)
+    L = 800
+    a = 1 + rng.integers(0, 128, d_c) / 128
+    Q, W_k = same_heads(H, d_c, [np.ones(d_c), a], (1.0, 2.0 ** -10))
+    rows, at = np.zeros((L, d_c)), 2 * rng.integers(0, d_c // 2, L)
+    rows[np.arange(L), at], rows[np.arange(L), at + 1] = 2.0 ** 12, -2.0 ** 12
+    got, want = weights_of(g, Q, rows, W_k, H)
+    assert want.max() > 3 * want.min()
+    assert (np.abs(got - want) <= EXACT * want).all()
