@@ -7,11 +7,11 @@
 //                  float16), with a float32 factor per (b, h): q~ = factor * f16, the
 //                  factor holding s and the power of two that brings the largest |f16| of
 //                  the d_c into [2^14, 2^15), so that neither the query's size nor the cache's
-//                  scale meets float16's ends.  If an element is not finite, nor is the factor
-//                  (NaN): every score of that head is NaN then
+//                  scale meets float16's ends.  If an element or s is not finite, nor is the
+//                  factor (NaN): every score of that head is NaN then
 //   bfloat16 parts hi = bf16(q~), lo = bf16(q~ - hi), for the accumulated attention
 //                  weights, whose float32 sums should not carry an 8-bit rounding of
-//                  the query: 17 bits; with few heads also third = bf16(q~ - hi - lo): 24
+//                  the query: 17 bits; with third = bf16(q~ - hi - lo) 24
 // One CTA per (head, 128 latent columns, 32 sequences): D[c, b] = A B with A =
 // 128 columns of W_k^(h) read MN-major, B = the 32 query rows (K-major), K = 128.
 // For float16 the CTAs of a head are a cluster (1, 2 or 4; a fourth without columns at
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(THREADS)
       sm.up[threadIdx.x] = __uint_as_float((uint32_t)(14 - e + 127) << 23);
       if (c0 == 0) {
         const float f = fminf(fmaxf(p.s * __uint_as_float((uint32_t)(e - 14 + 127) << 23), 0x1p-126f), 0x1.fffffep127f);
-        p.factor[(size_t)(b0 + threadIdx.x) * p.H + h] = top < 0x7f800000u ? f : __uint_as_float(0x7fffffffu);
+        p.factor[(size_t)(b0 + threadIdx.x) * p.H + h] = top < 0x7f800000u && isfinite(p.s) ? f : __uint_as_float(0x7fffffffu);
       }
     }
     __syncthreads();

@@ -4,11 +4,11 @@
 // cache_scale, so still with bfloat16's 8 significant bits):
 //   s = e4m3(max(min(max|x|, 2688) / 6, 2^-9)),   e_i = e2m1(x_i / s),
 // both rounded to nearest, ties to even.  The quotients are products with a float32
-// reciprocal, rounded to 16 significant bits: a half-way point m between two codes gives
-// m*s with at most 7 bits (and 6 m with 8 between two scales), so an x_i other than m*s
-// differs from it by 2^-8 relative or more, far outside both roundings, and an x_i equal
-// to m*s lands on m exactly and takes the even code.  The codes are therefore those of the
-// exact quotient.
+// reciprocal, the scale's rounded to 16 significant bits, a code's to a multiple of 2^-12: a
+// half-way point m between two codes (1/4 or more) gives m*s with at most 7 bits (and 6 m
+// with 8 between two scales), so an x_i other than m*s differs from it by 2^-8 relative or
+// more, far outside both roundings, and an x_i equal to m*s lands on m exactly and takes the
+// even code.  The codes are therefore those of the exact quotient.
 //
 // Both directions are bound by HBM: 2 bytes in and 9/16 byte out per value (or the
 // reverse).  524288 rows of 512 channels, 0.69 GB each way: stored in 104 us, read back in

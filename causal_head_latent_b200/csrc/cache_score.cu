@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       for (int j = 0; j < pc.n; ++j) {
         const TileSums sums = ring.next();
         float y[KT / 32][32];  // !FEW: the tile
-        if (!FEW) {  // the first of two sums is taken while the second grows, and both before the work on them
+        if (!FEW) {  // the first of two sums is taken while the second grows (of one, what is read here is not used)
           if (ring.two) ok = warp_wait(&d_full[sums.at[0]], sums.phase[0], p.status);
           tc_fence_after();
 #pragma unroll

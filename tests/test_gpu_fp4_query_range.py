@@ -121,3 +121,16 @@ def test_scores_that_all_overflow_are_not_an_empty_sequence(g):
     held = fp4_ref.values(codes.cpu().numpy(), scales.cpu().numpy())[1, 0].sum()
     assert np.isnan(got[0]).all()
     assert abs(got[1, 0] - held) <= 2.0 ** -8 * held and (got[1, 1:] == 0).all()
+
+
+@pytest.mark.parametrize("scale", [float("inf"), float("nan")])
+def test_a_score_scale_that_is_not_finite(g, scale):
+    rng = np.random.default_rng(9)
+    Q, rows = rand_rows(rng, 2, 256), rand_rows(rng, 2, 100, 64)
+    W_k, W_v = (rand_rows(rng, 256, 64) for _ in range(2))
+    codes, scales = empty_cache(2, 100, 64)
+    g.gmla_cache_quantize_fp4(rows, codes, scales)
+    O = torch.zeros(2, 256, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(g.gmla_attend_decode_fp4_workspace_size(2, 100, 2, 64), dtype=torch.uint8, device="cuda")
+    g.gmla_attend_decode_fp4(Q, codes, scales, 100, W_k, W_v, O, 2, scale=scale, workspace=ws)
+    assert torch.isnan(O).all()
