@@ -592,7 +592,7 @@ int launch_attend_fp4(const Fp4DecodeArgs &a, cudaStream_t stream) {
   if (!make_tmap_bf16(&tq, qt, 3, dq, sq, bq)) return -1;  // 2-byte elements, moved as they are
   const Params p{a.codes, a.scales, a.cache_len_max, a.H, a.dc, ShareBatch{a.lens, a.B, a.L, KT, kFp4PieceTiles}, qf, pm, pl, pacc, a.status};
   // Beginning beside the absorb kernel hides the set-up of a short launch (B=8 ragged to 16384:
-  // 72 us against 76), and slows a long one (B=32, L=131072: 0.96 ms against 0.89).
+  // 47.1 us against 48.5), and slows a long one (B=32, L=131072: 1.01 ms against 0.90).
   const long long tiles = (long long)a.B * ((a.L + KT - 1) / KT);
   if (launch_beside(tiles <= 32 * kShares, decode_kernel, dim3((unsigned)G), dim3(NUM_THREADS), smem_bytes(), stream, tq,
                     p) != 0)

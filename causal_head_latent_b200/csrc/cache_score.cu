@@ -600,8 +600,8 @@ static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t st
     p.S = reinterpret_cast<float *>(ws + lay.s);
     p.status = a.status;
     const long long G = share_count(nb, a.L, KT, kScorePieceTiles);
-    // Beginning beside a short launch hides 2 us (the sums at B=1, L=1001: 24.6 against 26.7); beside a
-    // long one it takes from its bandwidth (B=32, L=131072: 1.49 ms against 1.39).
+    // Beginning beside a short launch hides 4 us (B=1, L=1001: 20.6 against 24.7); beside a long one it takes
+    // from its bandwidth (B=32, L=131072: 1.47 ms against 1.37).
     const bool beside = p.tiles_max * nb <= 8 * kShares;
     if (launch_beside(beside && b0 == 0, scores_kernel<FEW, THIRD>, dim3((unsigned)G), dim3(NUM_THREADS), smem, stream, tq, tt, tc,
                       p) != 0)
@@ -616,9 +616,9 @@ static int launch_cache_score(const ScoreArgs &a, SmemSlot slot, cudaStream_t st
     // one tile per block until there are eight blocks per SM
     const long long per = p.tiles_max * nb / (8 * kShares);
     u.per_block = (int)(per < 1 ? 1 : per > 8 ? 8 : per);
-    // A few pieces per sequence are joined by every block that needs them (B=8, 19 pieces each: 51 us
-    // a call against 53); many cost less in a launch of their own (148 pieces: 41 us against 12 + 3 for
-    // one sequence of 131072 rows).
+    // A few pieces per sequence are joined by every block that needs them (B=8, ragged to 16384, 19 pieces
+    // each: 43 us a call against 45); many cost less in a launch of their own (one sequence of 131072 rows, 148
+    // pieces: 70 us against 85).
     u.lse = nullptr;
     if (G > 32ll * nb) {
       float *lse = reinterpret_cast<float *>(ws + lay.lse);
